@@ -369,6 +369,128 @@ DSA_API dsa_status_t dsa_selection_rows(const int32_t* idx, const int64_t* row_b
                                         int64_t* out, void* stream);
 DSA_API dsa_status_t dsa_sort_selection(int32_t* idx, float* score, int64_t rows, int32_t top_k, void* stream);
 
+/*
+ * The layer around the indexer.  A sparse-attention layer normalises its hidden rows to FP8, projects
+ * them, scores and selects with the indexer, appends the token's latent c^KV and rotated key part to a
+ * paged cache, and attends over the selected positions ("Study MLA Indexer", 数学流: the main attention is
+ * an MQA whose keys and values are the latents; its 两条 cache 区分 table: d_c = 512 per token;
+ * "Lightning Indexer 详解" §1: the core attention reads only the index set).  The projections are the
+ * caller's.  Every call below only enqueues on `stream`, can be captured in a CUDA graph, and reports
+ * faults found on the device through dsa_check_device_errors(stream).
+ */
+
+/*
+ * Root-mean-square norm of hidden rows with the residual's addition, quantised for FP8 projections:
+ *     s = x + residual;  y = s / sqrt(mean(s^2) + eps) * weight;  scale = absmax(y) / 448 (1 for zeros);
+ *     codes = E4M3(y / scale), round to nearest even, saturated
+ * in fp32 from the unrounded sum s.
+ *   x            device [rows, d] DSA_BF16 or DSA_F32 (dtype), rows x_stride elements apart (>= d)
+ *   residual     device [rows, d] of x's type, contiguous, or NULL (s = x)
+ *   residual_out device [rows, d] of x's type: s rounded to it; may be residual itself (NULL with it)
+ *   weight       device [d] DSA_BF16 or DSA_F32 (weight_dtype)
+ *   group        128: one scale per 128 values, scale [rows, ceil(d / 128)] (the last group may be
+ *                short); 0: one scale per row, scale [rows], as dsa_quantize_rows_fp8
+ *   normed       device [rows, d] bf16: y itself as well, or NULL
+ * d: a positive multiple of 16, at most 32768.  All pointers and rows 16-byte aligned (scale: 4).
+ * A NaN or infinity in a row spoils that row only.
+ */
+DSA_API dsa_status_t dsa_rmsnorm_fp8(const void* x, dsa_dtype_t dtype, int64_t x_stride, const void* residual,
+                                     void* residual_out, const void* weight, dsa_dtype_t weight_dtype, int64_t rows,
+                                     int32_t d, float eps, int32_t group, uint8_t* codes, float* scale, void* normed,
+                                     void* stream);
+
+/* The paged latent cache of one layer: num_pages pages of page_size rows, a row per token. */
+typedef struct {
+  void* latent;           /* device [num_pages * page_size, d_c] bf16 or E4M3 codes, 16-byte aligned     */
+  float* scale;           /* device [num_pages * page_size] fp32, a power of two per row (FP8), else NULL */
+  void* rope;             /* device [num_pages * page_size, d_r] bf16, 16-byte aligned; NULL for d_r = 0  */
+  int32_t num_pages;
+  int32_t page_size;      /* any positive size; num_pages * page_size < 2^31                             */
+  int32_t d_c;            /* 512                                                                         */
+  int32_t d_r;            /* 64, or 0: no rotated key part                                               */
+  dsa_dtype_t dtype;      /* of latent: DSA_BF16 or DSA_FP8_E4M3                                         */
+} dsa_latent_cache_t;
+
+/* Position p of sequence s lives in row pages[s * max_pages + p / page_size] * page_size + p % page_size.
+ * Entries outside [0, num_pages) mark pages that do not exist; reading or writing one is a device fault
+ * (the append skips the token, attention leaves the key out). */
+typedef struct {
+  const int32_t* pages;   /* device [num_seqs, max_pages] */
+  int32_t num_seqs;
+  int32_t max_pages;
+} dsa_page_table_t;
+
+/*
+ * Append n tokens: latent[row] = c_new (bf16, or E4M3 codes with a scale), rope[row] = kr_new rotated at the
+ * token's position (as dsa_indexer_kcache_append_rope rotates; rope_dim even, at most 64, in either pairing),
+ * row being that of position positions[i] of sequence seq_ids[i].  The FP8 scale is the smallest power of
+ * two with absmax <= 448 * scale, at least 2^-100 (1 for a row of zeros), so codes times scale are exact in
+ * bf16.
+ *   c_new     device [n, 512], rows c_stride elements apart (16-byte aligned), DSA_BF16 or DSA_F32
+ *   kr_new    device [n, 64], rows kr_stride elements apart, same type (not read for d_r = 0)
+ *   seq_ids   device int32 [n]; a negative one marks a padding token, which is skipped
+ *   positions device int32 [n]
+ * Two tokens of one call must not name the same position of the same page.  A sequence or position outside
+ * the page table is skipped and reported as a device fault.
+ */
+DSA_API dsa_status_t dsa_latent_append_rope(const dsa_latent_cache_t* cache, const dsa_page_table_t* pages,
+                                            const void* c_new, int64_t c_stride, const void* kr_new,
+                                            int64_t kr_stride, dsa_dtype_t src_dtype, const int32_t* seq_ids,
+                                            const int32_t* positions, int32_t n, const dsa_rope_t* rope, void* stream);
+
+/* Queries of the main attention in the latent's space (the key up-projection absorbed), and their rotated
+ * parts; bf16, strides in elements (multiples of 8), 16-byte aligned. */
+typedef struct {
+  const void* latent;     /* device [T, H, 512] */
+  int64_t latent_stride_t, latent_stride_h;
+  const void* rope;       /* device [T, H, 64]; not read for d_r = 0 */
+  int64_t rope_stride_t, rope_stride_h;
+  int32_t T;
+  int32_t H;              /* 1 .. 128 heads, all reading the same keys */
+} dsa_latent_query_t;
+
+/*
+ * Attention over a selection: for token t of sequence seq_ids[t], keys j = the entries idx[t, j] >= 0,
+ *     s[h, j] = sm_scale * (q.latent[t, h] . latent[row_j] + q.rope[t, h] . rope[row_j])
+ *     out[t, h] = sum_j softmax_j(s[h, j]) latent[row_j],   lse[t, h] = log sum_j exp(s[h, j])
+ *   idx      device int32 [T, top_k]: positions of the sequence, in any order, -1 anywhere for no entry (a
+ *            selection from prefill or decode); a position named twice counts twice
+ *   out      device [T, H, 512] bf16, contiguous, 16-byte aligned
+ *   lse      device fp32 [T, H] or NULL
+ * A token with no entry, or with a negative sequence (padding), gets zeros and -inf.  Scores, softmax
+ * statistics and sums are fp32; the weights are rounded to bf16 for their product with the latents.  The
+ * result is the same, bit for bit, on every run.
+ *   workspace  device, 256-byte aligned, dsa_sparse_attention_workspace_bytes(T, H, top_k) bytes (which may
+ *              be 0), used until the call's kernels finish; or NULL for the stream's own, grown with
+ *              cudaMalloc (graphs captured with NULL on one stream share it and must not run at the same
+ *              time).  dsa_set_workspace does not apply here.
+ */
+DSA_API dsa_status_t dsa_sparse_attention(const dsa_latent_query_t* q, const dsa_latent_cache_t* cache,
+                                          const dsa_page_table_t* pages, const int32_t* seq_ids, const int32_t* idx,
+                                          int32_t top_k, float sm_scale, void* out, float* lse, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
+/*
+ * Attention of a batch over every cached position, with a prefix that its sequences share computed once
+ * for all: token t reads positions 0 .. key_lens[t] - 1 of its sequence (key_lens[t] = its own position + 1
+ * for causal attention), positions below prefix_len through the page table's row prefix_seq.  The shared
+ * keys are read once for each 64 rows (token, head) of the whole batch; the rest per token.  prefix_len = 0
+ * is plain paged attention, the dense alternative while a sequence is no longer than top_k.
+ *   key_lens   device int32 [T], each at most max_keys (a longer one is cut there and reported); one below
+ *              prefix_len reads that many of the shared positions, one below 1 nothing (zeros and -inf)
+ *   max_keys   host bound on key_lens; the work is cut to it, so a tight one is faster
+ * The other arguments are those of dsa_sparse_attention; workspace: dsa_prefix_attention_workspace_bytes.
+ */
+DSA_API dsa_status_t dsa_prefix_attention(const dsa_latent_query_t* q, const dsa_latent_cache_t* cache,
+                                          const dsa_page_table_t* pages, const int32_t* seq_ids,
+                                          const int32_t* key_lens, int32_t prefix_len, int32_t prefix_seq,
+                                          int32_t max_keys, float sm_scale, void* out, float* lse, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of the two attention calls on the current device (0: none needed). */
+DSA_API size_t dsa_sparse_attention_workspace_bytes(int32_t T, int32_t H, int32_t top_k);
+DSA_API size_t dsa_prefix_attention_workspace_bytes(int32_t T, int32_t H, int32_t prefix_len, int32_t max_keys);
+
 /* Workspace bytes a call with this batch needs (scores plus scheduling tables). */
 DSA_API size_t dsa_indexer_workspace_bytes(const dsa_query_t* q, const dsa_batch_t* batch, int32_t top_k);
 

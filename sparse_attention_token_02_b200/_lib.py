@@ -35,6 +35,12 @@ EXPORTED = (
     "dsa_gather_rows",
     "dsa_selection_rows",
     "dsa_sort_selection",
+    "dsa_rmsnorm_fp8",
+    "dsa_latent_append_rope",
+    "dsa_sparse_attention",
+    "dsa_prefix_attention",
+    "dsa_sparse_attention_workspace_bytes",
+    "dsa_prefix_attention_workspace_bytes",
     "dsa_indexer_scores",
     "dsa_indexer_workspace_bytes",
     "dsa_set_workspace",
@@ -64,6 +70,22 @@ class Query(ctypes.Structure):
 class Batch(ctypes.Structure):
     _fields_ = [("num_seqs", ctypes.c_int32), ("seq_lens", ctypes.c_void_p), ("q_lens", ctypes.c_void_p),
                 ("k_base", ctypes.c_void_p)]
+
+
+class LatentCacheView(ctypes.Structure):
+    _fields_ = [("latent", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rope", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("d_c", ctypes.c_int32),
+                ("d_r", ctypes.c_int32), ("dtype", ctypes.c_int)]
+
+
+class PageTable(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("num_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
+class LatentQuery(ctypes.Structure):
+    _fields_ = [("latent", ctypes.c_void_p), ("latent_stride_t", ctypes.c_int64), ("latent_stride_h", ctypes.c_int64),
+                ("rope", ctypes.c_void_p), ("rope_stride_t", ctypes.c_int64), ("rope_stride_h", ctypes.c_int64),
+                ("T", ctypes.c_int32), ("H", ctypes.c_int32)]
 
 
 class DsaError(RuntimeError):
@@ -117,6 +139,22 @@ def load() -> ctypes.CDLL:
     lib.dsa_selection_rows.restype = st
     lib.dsa_sort_selection.argtypes = [V, V, I64, I32, V]
     lib.dsa_sort_selection.restype = st
+    F32 = ctypes.c_float
+    lib.dsa_rmsnorm_fp8.argtypes = [V, ctypes.c_int, I64, V, V, V, ctypes.c_int, I64, I32, F32, I32, V, V, V, V]
+    lib.dsa_rmsnorm_fp8.restype = st
+    lib.dsa_latent_append_rope.argtypes = [P(LatentCacheView), P(PageTable), V, I64, V, I64, ctypes.c_int, V, V, I32,
+                                           P(Rope), V]
+    lib.dsa_latent_append_rope.restype = st
+    lib.dsa_sparse_attention.argtypes = [P(LatentQuery), P(LatentCacheView), P(PageTable), V, V, I32, F32, V, V, V,
+                                         ctypes.c_size_t, V]
+    lib.dsa_sparse_attention.restype = st
+    lib.dsa_prefix_attention.argtypes = [P(LatentQuery), P(LatentCacheView), P(PageTable), V, V, I32, I32, I32, F32, V,
+                                         V, V, ctypes.c_size_t, V]
+    lib.dsa_prefix_attention.restype = st
+    lib.dsa_sparse_attention_workspace_bytes.argtypes = [I32, I32, I32]
+    lib.dsa_sparse_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.dsa_prefix_attention_workspace_bytes.argtypes = [I32, I32, I32, I32]
+    lib.dsa_prefix_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.dsa_indexer_scores.argtypes = [P(Query), P(KCache), V, P(Batch), V, I64, V]
     lib.dsa_indexer_scores.restype = st
     lib.dsa_indexer_workspace_bytes.argtypes = [P(Query), P(Batch), I32]

@@ -363,6 +363,215 @@ def dsa_sort_selection(idx, score, stream=None):
     return idx, score
 
 
+@dataclass
+class LatentCache:
+    """A paged latent cache: ``latent`` [pages * page_size, 512] bf16 or uint8 (E4M3 codes), ``rope``
+    [pages * page_size, 64] bf16 (None: no rotated key part), ``scale`` [pages * page_size] fp32 (FP8)."""
+    latent: torch.Tensor
+    rope: torch.Tensor | None
+    scale: torch.Tensor | None = None
+    page_size: int = 64
+
+    @staticmethod
+    def empty(num_pages: int, page_size: int = 64, fp8: bool = False, d_r: int = 64, device="cuda") -> "LatentCache":
+        rows = num_pages * page_size
+        return LatentCache(torch.zeros(rows, 512, dtype=torch.uint8 if fp8 else torch.bfloat16, device=device),
+                           torch.zeros(rows, d_r, dtype=torch.bfloat16, device=device) if d_r else None,
+                           torch.ones(rows, dtype=torch.float32, device=device) if fp8 else None, page_size)
+
+    @property
+    def fp8(self) -> bool:
+        return self.latent.dtype in (torch.uint8, torch.float8_e4m3fn)
+
+    def c(self) -> _lib.LatentCacheView:
+        _require_cuda(self.latent, self.rope, self.scale)
+        rows = self.latent.shape[0]
+        if self.page_size < 1 or rows % self.page_size:
+            raise ValueError("the cache must hold whole pages")
+        if not self.fp8 and self.latent.dtype != torch.bfloat16:
+            raise TypeError("latent must be bf16 or uint8 (E4M3 codes)")
+        if self.rope is not None and (self.rope.dtype != torch.bfloat16 or self.rope.shape[0] != rows):
+            raise ValueError("rope must be bf16 with a row for each latent row")
+        if self.fp8 and (self.scale is None or self.scale.dtype != torch.float32 or self.scale.numel() != rows):
+            raise ValueError("an FP8 latent cache needs one fp32 scale per row")
+        return _lib.LatentCacheView(self.latent.data_ptr(), self.scale.data_ptr() if self.scale is not None else None,
+                                    self.rope.data_ptr() if self.rope is not None else None, rows // self.page_size,
+                                    self.page_size, self.latent.shape[1], 0 if self.rope is None else self.rope.shape[1],
+                                    DSA_FP8_E4M3 if self.fp8 else DSA_BF16)
+
+
+def _on(first: torch.Tensor, stream, *others):
+    """(device guard, stream guard, stream): the calls below run on their tensors' device, and what they
+    allocate belongs to the stream that they launch on."""
+    for t in (first,) + others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}: one device is wanted")
+    if first.device.type != "cuda":
+        raise ValueError("device tensors must be CUDA tensors")
+    if stream is None:
+        stream = torch.cuda.current_stream(first.device)
+    elif stream.device != first.device:
+        raise ValueError(f"stream on {stream.device}, tensors on {first.device}")
+    return torch.cuda.stream(stream), ctypes.c_void_p(stream.cuda_stream)
+
+
+def _int32(name, t, *shape):
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def dsa_rmsnorm_fp8(x, weight, eps=1e-6, residual=None, group=128, residual_out=None, codes=None, scale=None,
+                    normed=None, stream=None):
+    """RMS norm of ``x`` [rows, d] (bf16 / fp32, rows may be strided) with the residual's addition, quantised to
+    E4M3: returns (codes uint8 [rows, d], scale fp32 [rows, ceil(d / 128)] or [rows, 1] with group=0,
+    residual_out or None).  ``residual_out`` may be ``residual`` itself; ``normed`` (bf16 [rows, d])
+    receives the unquantised rows too."""
+    if x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError("x must be [rows, d] with contiguous rows")
+    rows, d = x.shape
+    if weight.numel() != d:
+        raise ValueError("weight must hold d values")
+    if group not in (0, 128):
+        raise ValueError("group must be 0 (one scale per row) or 128")
+    guard, st = _on(x, stream, weight, residual, residual_out, codes, scale, normed)
+    with guard:
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty(rows, d, dtype=residual.dtype, device=x.device)
+        if codes is None:
+            codes = torch.empty(rows, d, dtype=torch.uint8, device=x.device)
+        if scale is None:
+            scale = torch.empty(rows, -(-d // 128) if group else 1, dtype=torch.float32, device=x.device)
+        _require_cuda(weight, residual, residual_out, codes, scale, normed)
+        for name, t, dt, n in (("residual", residual, (x.dtype,), rows * d), ("residual_out", residual_out, (x.dtype,), rows * d),
+                               ("codes", codes, (torch.uint8, torch.float8_e4m3fn), rows * d),
+                               ("scale", scale, (torch.float32,), rows * (-(-d // 128) if group else 1)),
+                               ("normed", normed, (torch.bfloat16,), rows * d)):
+            if t is not None and t.dtype not in dt:
+                raise TypeError(f"{name} must be {dt[0]}")
+            if t is not None and t.numel() != n:
+                raise ValueError(f"{name} must hold {n} values")
+        check(_lib.load().dsa_rmsnorm_fp8(_ptr(x), _dtype_code(x), x.stride(0), _ptr(residual), _ptr(residual_out),
+                                          _ptr(weight), _dtype_code(weight), rows, d, float(eps), int(group),
+                                          _ptr(codes), _ptr(scale), _ptr(normed), st))
+    return codes, scale, residual_out
+
+
+def _page_table(page_table) -> _lib.PageTable:
+    if page_table.dim() != 2 or page_table.dtype != torch.int32:
+        raise TypeError("page_table must be int32 [num_seqs, max_pages]")
+    _require_cuda(page_table)
+    return _lib.PageTable(page_table.data_ptr(), page_table.shape[0], page_table.shape[1])
+
+
+def dsa_latent_append_rope(cache: LatentCache, page_table, c_new, kr_new, seq_ids, positions, rope_dim=None,
+                           base=10000.0, interleaved=True, stream=None):
+    """Append tokens to a paged latent cache: latents ``c_new`` [n, 512] and pre-RoPE key parts ``kr_new`` [n, 64]
+    (bf16 / fp32, rows may be strided; None for a cache without a rotated part) of positions ``positions`` (int32 [n]) of
+    sequences ``seq_ids`` (int32 [n], negative: a padding token).  ``page_table`` int32 [num_seqs, max_pages]."""
+    n = c_new.shape[0]
+    for name, t, width in (("c_new", c_new, 512), ("kr_new", kr_new, 64)):
+        if t is None and name == "kr_new" and cache.rope is None:
+            continue
+        if t is None or t.dim() != 2 or t.shape[0] != n or t.shape[1] != width or (n and t.stride(1) != 1):
+            raise ValueError(f"{name} must be [n, {width}] with contiguous rows")
+    if kr_new is not None and kr_new.dtype != c_new.dtype:
+        raise TypeError("c_new and kr_new must have one dtype")
+    _int32("seq_ids", seq_ids, n)
+    _int32("positions", positions, n)
+    _require_cuda(seq_ids, positions)
+    guard, st = _on(cache.latent, stream, cache.rope, cache.scale, page_table, c_new, kr_new, seq_ids, positions)
+    cc, pt, r = cache.c(), _page_table(page_table), _rope(64, rope_dim, base, interleaved)
+    with guard:
+        check(_lib.load().dsa_latent_append_rope(ctypes.byref(cc), ctypes.byref(pt), _ptr(c_new), c_new.stride(0),
+                                                 _ptr(kr_new), 0 if kr_new is None else kr_new.stride(0),
+                                                 _dtype_code(c_new), _ptr(seq_ids), _ptr(positions), n, ctypes.byref(r),
+                                                 st))
+
+
+def _attend(call, q_latent, q_rope, cache, page_table, out, lse, stream, workspace, workspace_bytes, *ints):
+    for name, t, width in (("q_latent", q_latent, 512), ("q_rope", q_rope, 64)):
+        if t is None and name == "q_rope" and cache.rope is None:
+            continue
+        if t is None or t.dim() != 3 or t.shape[2] != width or t.shape[:2] != q_latent.shape[:2]:
+            raise ValueError(f"{name} must be [T, H, {width}]")
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be bf16")
+        if t.numel() and t.stride(2) != 1:
+            raise ValueError(f"{name} must be contiguous in its last dimension")
+    T, H, _ = q_latent.shape
+    _require_cuda(*ints)
+    guard, st = _on(q_latent, stream, q_rope, cache.latent, cache.rope, cache.scale, page_table, out, lse, workspace, *ints)
+    cc, pt = cache.c(), _page_table(page_table)
+    qr = (0, 0, 0) if q_rope is None else (q_rope.data_ptr(), q_rope.stride(0), q_rope.stride(1))
+    qq = _lib.LatentQuery(q_latent.data_ptr(), q_latent.stride(0), q_latent.stride(1), *qr, T, H)
+    with guard:
+        if out is None:
+            out = torch.empty(T, H, 512, dtype=torch.bfloat16, device=q_latent.device)
+        if lse is None:
+            lse = torch.empty(T, H, dtype=torch.float32, device=q_latent.device)
+        _require_cuda(out, lse, workspace)
+        if out.dtype != torch.bfloat16 or lse.dtype != torch.float32:
+            raise TypeError("out must be bf16 and lse fp32")
+        if out.numel() != T * H * 512 or lse.numel() != T * H:
+            raise ValueError("out must be [T, H, 512] and lse [T, H]")
+        if workspace is None:
+            # from torch's allocator, so that a captured graph keeps its own
+            need = workspace_bytes(T, H)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q_latent.device) if need else None
+        ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        check(call(ctypes.byref(qq), ctypes.byref(cc), ctypes.byref(pt), _ptr(out), _ptr(lse), _ptr(workspace), ws, st))
+    return out, lse
+
+
+def dsa_sparse_attention(q_latent, q_rope, cache: LatentCache, page_table, seq_ids, idx, sm_scale, out=None, lse=None,
+                         workspace=None, stream=None):
+    """Attention over a selection: queries ``q_latent`` [T, H, 512] and ``q_rope`` [T, H, 64] (bf16, any strides of
+    whole 16-byte vectors; q_rope None for a cache without a rotated part) of sequences ``seq_ids`` (int32 [T], negative:
+    padding) over the positions ``idx`` (int32 [T, k], -1: no entry) of the paged cache.  Returns (out bf16
+    [T, H, 512], lse fp32 [T, H]).  ``workspace``: uint8 of dsa_sparse_attention_workspace_bytes (default: allocated)."""
+    lib, T = _lib.load(), q_latent.shape[0]
+    if idx.dim() != 2:
+        raise ValueError("idx must be [T, k]")
+    _int32("seq_ids", seq_ids, T)
+    _int32("idx", idx, T, idx.shape[1])
+    k = idx.shape[1]
+
+    def call(q, c, p, o, l, w, n, st):
+        return lib.dsa_sparse_attention(q, c, p, _ptr(seq_ids), _ptr(idx), k, float(sm_scale), o, l, w, n, st)
+
+    return _attend(call, q_latent, q_rope, cache, page_table, out, lse, stream, workspace,
+                   lambda t, h: lib.dsa_sparse_attention_workspace_bytes(t, h, k), seq_ids, idx)
+
+
+def dsa_prefix_attention(q_latent, q_rope, cache: LatentCache, page_table, seq_ids, key_lens, sm_scale, prefix_len=0,
+                         prefix_seq=0, max_keys=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention over every cached position below ``key_lens`` (int32 [T]), the first ``prefix_len`` shared by the whole
+    batch and read once, through row ``prefix_seq`` of the page table.  ``max_keys`` bounds key_lens (default: what the
+    page table can hold).  Other arguments and results as dsa_sparse_attention."""
+    lib, T = _lib.load(), q_latent.shape[0]
+    _int32("seq_ids", seq_ids, T)
+    _int32("key_lens", key_lens, T)
+    if max_keys is None:
+        max_keys = page_table.shape[1] * cache.page_size
+    m, p0, s0 = int(max_keys), int(prefix_len), int(prefix_seq)
+
+    def call(q, c, p, o, l, w, n, st):
+        return lib.dsa_prefix_attention(q, c, p, _ptr(seq_ids), _ptr(key_lens), p0, s0, m, float(sm_scale), o, l, w, n, st)
+
+    return _attend(call, q_latent, q_rope, cache, page_table, out, lse, stream, workspace,
+                   lambda t, h: lib.dsa_prefix_attention_workspace_bytes(t, h, p0, m), seq_ids, key_lens)
+
+
+def dsa_sparse_attention_workspace_bytes(T: int, H: int, top_k: int) -> int:
+    return int(_lib.load().dsa_sparse_attention_workspace_bytes(T, H, top_k))
+
+
+def dsa_prefix_attention_workspace_bytes(T: int, H: int, prefix_len: int, max_keys: int) -> int:
+    return int(_lib.load().dsa_prefix_attention_workspace_bytes(T, H, prefix_len, max_keys))
+
+
 def dsa_indexer_scores(q, cache: IndexerKCache, w, seq_lens, q_scale=None, q_lens=None, k_base=None, ld=None,
                        out=None, stream=None):
     """Dense scores [T_total, ld] (entries after each query's position are left as they were: -inf here)."""

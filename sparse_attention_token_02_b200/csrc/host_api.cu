@@ -155,10 +155,33 @@ struct Ctx {
   StepSlot step[2];
   int step_next = 0;
   cudaStream_t copy_in = nullptr, copy_out = nullptr;
+  // attention over the latent cache: the parts of calls that bring no workspace of their own
+  void* d_attn = nullptr;
+  size_t attn_cap = 0;
+  bool attn_frozen = false;       // a captured graph reads d_attn
 };
 
 std::mutex g_mu;
 std::map<std::pair<int, cudaStream_t>, Ctx*> g_ctx;
+
+// Lets this thread allocate while a stream of it is being captured: a first call on a stream may come
+// inside a capture, and what it allocates outlives the graph.
+struct AllowAllocation {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  AllowAllocation() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~AllowAllocation() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
+// Zeroes device memory without touching the legacy stream, which a capture may forbid.
+cudaError_t zero_now(void* p, size_t bytes) {
+  cudaStream_t s = nullptr;
+  cudaError_t e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+  if (e != cudaSuccess) return e;
+  e = cudaMemsetAsync(p, 0, bytes, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  cudaStreamDestroy(s);
+  return e;
+}
 
 dsa_status_t get_ctx(cudaStream_t stream, Ctx** out) {
   int dev = 0;
@@ -170,6 +193,7 @@ dsa_status_t get_ctx(cudaStream_t stream, Ctx** out) {
     *out = it->second;
     return DSA_OK;
   }
+  AllowAllocation allow;
   Ctx* c = new Ctx();
   c->device = dev;
   c->stream = stream;
@@ -178,7 +202,7 @@ dsa_status_t get_ctx(cudaStream_t stream, Ctx** out) {
     delete c;
     return fail(DSA_ERR_ALLOC, "cudaMalloc(error flag): %s", cudaGetErrorString(e));
   }
-  e = cudaMemset(c->d_err, 0, 2 * sizeof(int));
+  e = zero_now(c->d_err, 2 * sizeof(int));
   if (e != cudaSuccess) return cuda_fail(e, "cudaMemset(error flag)");
   for (int i = 0; i < kRing; ++i) {
     e = cudaEventCreateWithFlags(&c->h_event[i], cudaEventDisableTiming);
@@ -1242,6 +1266,7 @@ dsa_status_t dsa_check_device_errors(void* stream_v) {
   const char* what = h[0] == DSA_DEVERR_TIMEOUT ? "a bounded wait expired in block"
                      : h[0] == DSA_DEVERR_BOUNDS ? "cache append destination out of range for source row"
                      : h[0] == DSA_DEVERR_TOPK   ? "top-k selection invariant broken on row"
+                     : h[0] == DSA_DEVERR_PAGE   ? "sequence, position or length outside the page table for token"
                                                  : "unknown device fault, info";
   return fail(DSA_ERR_DEVICE_CHECK, "device fault %d: %s %d", h[0], what, h[1]);
 }
@@ -1258,6 +1283,263 @@ uint64_t dsa_kernel_launch_count(void) { return g_launches; }
 const char* dsa_get_last_error(void) { return g_last_error.c_str(); }
 
 const char* dsa_version(void) { return "dsa_indexer 0.1 (sm_100a)"; }
+
+}  // extern "C"
+
+// ============================================================================= the layer's operators
+//
+// What a sparse-attention layer runs beside the indexer: the norm that makes its FP8 rows, the paged
+// latent cache's append, and the attention that reads that cache, over a selection or over every
+// position with a prefix that the batch shares.
+
+namespace dsa {
+namespace {
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+dsa_status_t check_latent(const dsa_latent_cache_t* c, const dsa_page_table_t* t, LatentView* v) {
+  if (!c || !t) return fail(DSA_ERR_INVALID_ARG, "latent cache or page table is NULL");
+  if (!c->latent || !t->pages) return fail(DSA_ERR_INVALID_ARG, "latent cache or page table has a NULL pointer");
+  if (c->dtype != DSA_BF16 && c->dtype != DSA_FP8_E4M3)
+    return fail(DSA_ERR_INVALID_ARG, "latent cache dtype must be DSA_BF16 or DSA_FP8_E4M3");
+  if (c->dtype == DSA_FP8_E4M3 && !c->scale) return fail(DSA_ERR_INVALID_ARG, "FP8 latent cache needs scale");
+  if (c->d_c != kLatentDim) return fail(DSA_ERR_UNSUPPORTED, "d_c must be %d (got %d)", kLatentDim, c->d_c);
+  if (c->d_r != 0 && c->d_r != kLatentRope) return fail(DSA_ERR_UNSUPPORTED, "d_r must be 0 or %d (got %d)", kLatentRope, c->d_r);
+  if (c->d_r && !c->rope) return fail(DSA_ERR_INVALID_ARG, "latent cache with d_r needs rope");
+  if (c->num_pages < 1 || c->page_size < 1 || int64_t(c->num_pages) * c->page_size >= (int64_t(1) << 31))
+    return fail(DSA_ERR_INVALID_ARG, "num_pages and page_size must be positive and hold fewer than 2^31 rows");
+  if (t->num_seqs < 1 || t->max_pages < 1) return fail(DSA_ERR_INVALID_ARG, "page table must have at least one row and one column");
+  if (!aligned16(c->latent) || !aligned16(c->rope)) return fail(DSA_ERR_INVALID_ARG, "latent and rope must be 16-byte aligned");
+  *v = LatentView{c->latent, c->dtype == DSA_FP8_E4M3 ? c->scale : nullptr, c->d_r ? c->rope : nullptr, c->num_pages,
+                  c->page_size, c->dtype == DSA_FP8_E4M3, t->pages, t->num_seqs, t->max_pages};
+  return DSA_OK;
+}
+
+// Query strides: vectors of 8 bf16 must stay 16-byte aligned.
+dsa_status_t check_latent_query(const dsa_latent_query_t* q, const LatentView& v) {
+  if (!q->latent || (v.rope && !q->rope)) return fail(DSA_ERR_INVALID_ARG, "query has a NULL pointer");
+  if (q->H < 1 || q->H > 128) return fail(DSA_ERR_UNSUPPORTED, "H must be in 1 .. 128 (got %d)", q->H);
+  if (int64_t(q->T) * q->H >= (int64_t(1) << 30)) return fail(DSA_ERR_UNSUPPORTED, "too many query rows for one call");
+  const bool many = q->T > 1, heads = q->H > 1;       // a stride that no row uses may be anything
+  if (!aligned16(q->latent) || (many && q->latent_stride_t % 8) || (heads && q->latent_stride_h % 8))
+    return fail(DSA_ERR_INVALID_ARG, "query latents must be 16-byte aligned with strides in multiples of 8 values");
+  if (v.rope && (!aligned16(q->rope) || (many && q->rope_stride_t % 8) || (heads && q->rope_stride_h % 8)))
+    return fail(DSA_ERR_INVALID_ARG, "query rope parts must be 16-byte aligned with strides in multiples of 8 values");
+  return DSA_OK;
+}
+
+int current_sms() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
+  return num_sms(dev);
+}
+
+// Workspace of one attention call: the caller's, or the stream's own.
+dsa_status_t attention_parts(Ctx* c, size_t need, void* workspace, size_t workspace_bytes, void** out) {
+  *out = nullptr;
+  if (need == 0) return DSA_OK;
+  if (workspace) {
+    if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(DSA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    if (workspace_bytes < need)
+      return fail(DSA_ERR_ALLOC, "workspace holds %zu bytes, this call needs %zu", workspace_bytes, need);
+    *out = workspace;
+    return DSA_OK;
+  }
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  DSA_CUDA_TRY(cudaStreamIsCapturing(c->stream, &cap), "cudaStreamIsCapturing");
+  const bool capturing = cap != cudaStreamCaptureStatusNone;
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (need > c->attn_cap) {
+    AllowAllocation allow;
+    if (c->d_attn) {
+      if (c->attn_frozen || capturing) {              // a graph may read it, or work that cannot be waited for
+        c->graveyard.push_back(c->d_attn);
+      } else {
+        DSA_CUDA_TRY(cudaStreamSynchronize(c->stream), "cudaStreamSynchronize");
+        cudaFree(c->d_attn);
+      }
+    }
+    c->d_attn = nullptr;
+    c->attn_cap = 0;
+    c->attn_frozen = false;
+    const size_t bytes = align_up(std::max(need + need / 8, size_t(1) << 20));
+    cudaError_t e = cudaMalloc(&c->d_attn, bytes);
+    if (e != cudaSuccess) return fail(DSA_ERR_ALLOC, "cudaMalloc(%zu) for attention parts: %s", bytes, cudaGetErrorString(e));
+    c->attn_cap = bytes;
+  }
+  if (capturing) c->attn_frozen = true;
+  *out = c->d_attn;
+  return DSA_OK;
+}
+
+dsa_status_t run_attention(const dsa_latent_query_t* q, AttnArgs* a, int64_t shared_keys, int64_t own_keys, float sm_scale,
+                           void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream_v) {
+  if (!out) return fail(DSA_ERR_INVALID_ARG, "out is NULL");
+  if (!aligned16(out)) return fail(DSA_ERR_INVALID_ARG, "out must be 16-byte aligned");
+  if (!std::isfinite(sm_scale)) return fail(DSA_ERR_INVALID_ARG, "sm_scale must be finite");
+  a->q_latent = q->latent;
+  a->ql_t = q->latent_stride_t;
+  a->ql_h = q->latent_stride_h;
+  a->q_rope = q->rope;
+  a->qr_t = q->rope_stride_t;
+  a->qr_h = q->rope_stride_h;
+  a->T = q->T;
+  a->H = q->H;
+  a->scale_log2 = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
+  a->out = out;
+  a->lse = lse;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+  Ctx* c = nullptr;
+  dsa_status_t st = get_ctx(stream, &c);
+  if (st != DSA_OK) return st;
+  const AttnPlan p = plan_attention(q->T, q->H, shared_keys, own_keys, current_sms());
+  void* ws = nullptr;
+  if ((st = attention_parts(c, attention_workspace(p, q->T, q->H), workspace, workspace_bytes, &ws)) != DSA_OK) return st;
+  a->part_o = static_cast<float*>(ws);
+  a->part_lse = a->part_o ? a->part_o + size_t(p.slots()) * q->T * q->H * kLatentDim : nullptr;
+  a->err = c->d_err;
+  int launched = 0;
+  const cudaError_t e = launch_attention(*a, p, &launched, stream);
+  g_launches += launched;
+  if (e != cudaSuccess) return cuda_fail(e, "attention kernel launch");
+  return DSA_OK;
+}
+
+constexpr int32_t kMaxKeys = 1 << 30;
+
+}  // namespace
+}  // namespace dsa
+
+extern "C" {
+
+dsa_status_t dsa_rmsnorm_fp8(const void* x, dsa_dtype_t dtype, int64_t x_stride, const void* residual, void* residual_out,
+                             const void* weight, dsa_dtype_t weight_dtype, int64_t rows, int32_t d, float eps, int32_t group,
+                             uint8_t* codes, float* scale, void* normed, void* stream_v) {
+  g_last_error.clear();
+  if (rows < 0) return fail(DSA_ERR_INVALID_ARG, "rows < 0");
+  if (d <= 0 || d % 16) return fail(DSA_ERR_INVALID_ARG, "d must be a positive multiple of 16");
+  if (d > kNormMaxD) return fail(DSA_ERR_UNSUPPORTED, "d must be at most %d", kNormMaxD);
+  if (group != 0 && group != 128) return fail(DSA_ERR_UNSUPPORTED, "group must be 0 (one scale per row) or 128");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(DSA_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (dtype != DSA_BF16 && dtype != DSA_F32) return fail(DSA_ERR_INVALID_ARG, "dtype must be DSA_BF16 or DSA_F32");
+  if (weight_dtype != DSA_BF16 && weight_dtype != DSA_F32)
+    return fail(DSA_ERR_INVALID_ARG, "weight_dtype must be DSA_BF16 or DSA_F32");
+  if (rows == 0) return DSA_OK;
+  if (rows > 0x7FFFFFFF) return fail(DSA_ERR_UNSUPPORTED, "too many rows for one launch");
+  if (!x || !weight || !codes || !scale) return fail(DSA_ERR_INVALID_ARG, "a required pointer is NULL");
+  if (!residual != !residual_out) return fail(DSA_ERR_INVALID_ARG, "residual and residual_out go together");
+  const int64_t esz = dtype == DSA_F32 ? 4 : 2;
+  if (rows > 1 && x_stride < d) return fail(DSA_ERR_INVALID_ARG, "x_stride must be at least d");
+  if (!aligned16(x) || (rows > 1 && x_stride * esz % 16) || !aligned16(residual) || !aligned16(residual_out) ||
+      !aligned16(weight) || !aligned16(codes) || !aligned16(normed))
+    return fail(DSA_ERR_INVALID_ARG, "rows, weight, codes and normed must be 16-byte aligned");
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+  Ctx* c = nullptr;
+  dsa_status_t st = get_ctx(stream, &c);
+  if (st != DSA_OK) return st;
+  const NormArgs a{x, x_stride, residual, residual_out, weight, dtype == DSA_F32, weight_dtype == DSA_F32,
+                   rows, d, eps, group, codes, scale, normed};
+  DSA_CUDA_TRY(launch_rmsnorm_fp8(a, stream), "norm kernel launch");
+  ++g_launches;
+  return DSA_OK;
+}
+
+dsa_status_t dsa_latent_append_rope(const dsa_latent_cache_t* cache, const dsa_page_table_t* pages, const void* c_new,
+                                    int64_t c_stride, const void* kr_new, int64_t kr_stride, dsa_dtype_t src_dtype,
+                                    const int32_t* seq_ids, const int32_t* positions, int32_t n, const dsa_rope_t* rope,
+                                    void* stream_v) {
+  g_last_error.clear();
+  LatentAppendArgs a{};
+  dsa_status_t st = check_latent(cache, pages, &a.kv);
+  if (st != DSA_OK) return st;
+  if (n < 0) return fail(DSA_ERR_INVALID_ARG, "n < 0");
+  if (src_dtype != DSA_BF16 && src_dtype != DSA_F32) return fail(DSA_ERR_INVALID_ARG, "src_dtype must be DSA_BF16 or DSA_F32");
+  RopeParams rp{};
+  if (a.kv.rope) {
+    if (!rope) return fail(DSA_ERR_INVALID_ARG, "rope is NULL");
+    if (rope->rope_dim < 0 || rope->rope_dim % 2 || rope->rope_dim > kLatentRope)
+      return fail(DSA_ERR_UNSUPPORTED, "rope_dim must be even and at most %d", kLatentRope);
+    if (rope->rope_dim && !(rope->base > 0.0 && std::isfinite(rope->base)))
+      return fail(DSA_ERR_INVALID_ARG, "rope base must be positive and finite");
+    rp = rope_params(*rope);
+  }
+  if (n == 0) return DSA_OK;
+  if (!c_new || !seq_ids || !positions || (a.kv.rope && !kr_new)) return fail(DSA_ERR_INVALID_ARG, "a required pointer is NULL");
+  const int64_t esz = src_dtype == DSA_F32 ? 4 : 2;
+  if (!aligned16(c_new) || (n > 1 && c_stride * esz % 16))
+    return fail(DSA_ERR_INVALID_ARG, "rows of c_new must be 16-byte aligned");
+  if (n > 1 && (c_stride < kLatentDim || (a.kv.rope && kr_stride < kLatentRope)))
+    return fail(DSA_ERR_INVALID_ARG, "row strides must be at least the row lengths");
+  a.c_new = c_new;
+  a.c_stride = c_stride;
+  a.kr_new = kr_new;
+  a.kr_stride = kr_stride;
+  a.src_f32 = src_dtype == DSA_F32;
+  a.seq_ids = seq_ids;
+  a.positions = positions;
+  a.n = n;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+  Ctx* c = nullptr;
+  if ((st = get_ctx(stream, &c)) != DSA_OK) return st;
+  a.err = c->d_err;
+  DSA_CUDA_TRY(launch_latent_append(a, rp, stream), "latent append kernel launch");
+  ++g_launches;
+  return DSA_OK;
+}
+
+dsa_status_t dsa_sparse_attention(const dsa_latent_query_t* q, const dsa_latent_cache_t* cache, const dsa_page_table_t* pages,
+                                  const int32_t* seq_ids, const int32_t* idx, int32_t top_k, float sm_scale, void* out,
+                                  float* lse, void* workspace, size_t workspace_bytes, void* stream_v) {
+  g_last_error.clear();
+  AttnArgs a{};
+  dsa_status_t st = check_latent(cache, pages, &a.kv);
+  if (st != DSA_OK) return st;
+  if (!q) return fail(DSA_ERR_INVALID_ARG, "query is NULL");
+  if (q->T < 0) return fail(DSA_ERR_INVALID_ARG, "T < 0");
+  if (top_k < 1 || top_k > kMaxKeys) return fail(DSA_ERR_INVALID_ARG, "top_k must be in 1 .. 2^30");
+  if (q->T == 0) return DSA_OK;
+  if ((st = check_latent_query(q, a.kv)) != DSA_OK) return st;
+  if (!seq_ids || !idx) return fail(DSA_ERR_INVALID_ARG, "seq_ids or idx is NULL");
+  a.seq_ids = seq_ids;
+  a.idx = idx;
+  a.top_k = top_k;
+  return run_attention(q, &a, 0, top_k, sm_scale, out, lse, workspace, workspace_bytes, stream_v);
+}
+
+dsa_status_t dsa_prefix_attention(const dsa_latent_query_t* q, const dsa_latent_cache_t* cache, const dsa_page_table_t* pages,
+                                  const int32_t* seq_ids, const int32_t* key_lens, int32_t prefix_len, int32_t prefix_seq,
+                                  int32_t max_keys, float sm_scale, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream_v) {
+  g_last_error.clear();
+  AttnArgs a{};
+  dsa_status_t st = check_latent(cache, pages, &a.kv);
+  if (st != DSA_OK) return st;
+  if (!q) return fail(DSA_ERR_INVALID_ARG, "query is NULL");
+  if (q->T < 0) return fail(DSA_ERR_INVALID_ARG, "T < 0");
+  if (prefix_len < 0 || max_keys < prefix_len || max_keys > kMaxKeys)
+    return fail(DSA_ERR_INVALID_ARG, "need 0 <= prefix_len (%d) <= max_keys (%d) <= 2^30", prefix_len, max_keys);
+  if (prefix_len > 0 && (prefix_seq < 0 || prefix_seq >= a.kv.num_seqs))
+    return fail(DSA_ERR_INVALID_ARG, "prefix_seq %d is not a row of the page table", prefix_seq);
+  if (q->T == 0) return DSA_OK;
+  if ((st = check_latent_query(q, a.kv)) != DSA_OK) return st;
+  if (!seq_ids || !key_lens) return fail(DSA_ERR_INVALID_ARG, "seq_ids or key_lens is NULL");
+  a.seq_ids = seq_ids;
+  a.key_lens = key_lens;
+  a.shared_len = prefix_len;
+  a.shared_seq = prefix_seq;
+  a.max_keys = max_keys;
+  return run_attention(q, &a, prefix_len, max_keys - prefix_len, sm_scale, out, lse, workspace, workspace_bytes, stream_v);
+}
+
+size_t dsa_sparse_attention_workspace_bytes(int32_t T, int32_t H, int32_t top_k) {
+  if (T < 1 || H < 1 || H > 128 || top_k < 1 || top_k > kMaxKeys) return 0;
+  return attention_workspace(plan_attention(T, H, 0, top_k, current_sms()), T, H);
+}
+
+size_t dsa_prefix_attention_workspace_bytes(int32_t T, int32_t H, int32_t prefix_len, int32_t max_keys) {
+  if (T < 1 || H < 1 || H > 128 || prefix_len < 0 || max_keys < prefix_len || max_keys > kMaxKeys) return 0;
+  return attention_workspace(plan_attention(T, H, prefix_len, max_keys - prefix_len, current_sms()), T, H);
+}
 
 }  // extern "C"
 

@@ -13,6 +13,7 @@ enum : int {
   DSA_DEVERR_TIMEOUT = 1,     // a bounded wait ran out
   DSA_DEVERR_BOUNDS = 2,      // a destination row outside the cache capacity
   DSA_DEVERR_TOPK = 3,        // selection invariant broken (count mismatch)
+  DSA_DEVERR_PAGE = 4,        // a token's sequence, position or length outside its page table
 };
 
 constexpr int kKeyTile = 128;       // keys per UMMA tile (the M dimension)
@@ -157,6 +158,91 @@ cudaError_t launch_quantize_rows_fp8(const void* src, int src_is_f32, int64_t ro
                                      int* err, cudaStream_t stream);
 cudaError_t launch_append_bf16(const void* src, int src_is_f32, int64_t rows, int32_t row_len, uint16_t* dst,
                                const int64_t* dst_rows, int64_t dst_capacity, int* err, cudaStream_t stream);
+
+// ----------------------------------------------------------------------------- the layer's operators
+
+// RMS norm with the residual's addition and FP8 output.
+constexpr int32_t kNormMaxD = 32768;
+struct NormArgs {
+  const void* x;               // [rows, d], rows x_stride elements apart, bf16 or fp32
+  int64_t x_stride;
+  const void* residual;        // [rows, d] of x's type, or nullptr
+  void* residual_out;          // [rows, d] of x's type (set with residual)
+  const void* weight;          // [d] bf16 or fp32
+  int x_f32, w_f32;
+  int64_t rows;
+  int32_t d;
+  float eps;
+  int32_t group;               // values per scale: 128, or 0 for the whole row
+  uint8_t* codes;              // [rows, d]
+  float* scale;                // [rows, ceil(d / group)] ([rows] for group 0)
+  void* normed;                // [rows, d] bf16, or nullptr
+};
+cudaError_t launch_rmsnorm_fp8(const NormArgs& a, cudaStream_t stream);
+
+// The paged latent cache.  Row of position p of sequence s:
+//   pages[s * max_pages + p / page_size] * page_size + p % page_size.
+constexpr int kLatentDim = 512;        // latent values per token
+constexpr int kLatentRope = 64;        // rotated key values per token (or none)
+struct LatentView {
+  void* latent;                // [num_pages * page_size, 512] bf16 or E4M3
+  float* scale;                // [num_pages * page_size] (FP8)
+  void* rope;                  // [num_pages * page_size, 64] bf16, or nullptr
+  int32_t num_pages, page_size;
+  int32_t fp8;
+  const int32_t* pages;        // [num_seqs, max_pages]
+  int32_t num_seqs, max_pages;
+};
+struct LatentAppendArgs {
+  LatentView kv;
+  const void* c_new;           // [n, 512] rows c_stride elements apart, bf16 or fp32
+  int64_t c_stride;
+  const void* kr_new;          // [n, 64] rows kr_stride elements apart, same type
+  int64_t kr_stride;
+  int src_f32;
+  const int32_t* seq_ids;
+  const int32_t* positions;
+  int32_t n;
+  int* err;
+};
+cudaError_t launch_latent_append(const LatentAppendArgs& a, const RopeParams& r, cudaStream_t stream);
+
+// Attention over the latent cache: out[t, h] = sum_j softmax_j(scale * q . k_j) c_j.
+// How a call is cut: a work item is up to kAttnRows rows (token, head) against a range of keys.
+// Shared items: rows of the whole batch, packed, against chunk `slot` of the shared prefix.
+// Own items: rows of one token against chunk `slot` of that token's own keys.
+constexpr int kAttnRows = 64;          // rows per work item
+constexpr int kAttnTile = 64;          // keys per tile; chunks are whole tiles
+struct AttnPlan {
+  int32_t shared_groups, shared_slots, shared_chunk;
+  int32_t own_groups, own_slots, own_chunk;       // own_groups: row groups of one token
+  __host__ __device__ int32_t slots() const { return shared_slots + own_slots; }
+};
+struct AttnArgs {
+  LatentView kv;
+  const void* q_latent;        // bf16, strides in elements
+  int64_t ql_t, ql_h;
+  const void* q_rope;
+  int64_t qr_t, qr_h;
+  int32_t T, H;
+  const int32_t* seq_ids;      // [T]; negative: a padding token
+  const int32_t* idx;          // [T, top_k] positions, or nullptr: every position below key_lens
+  int32_t top_k;
+  const int32_t* key_lens;     // [T]
+  int32_t shared_len, shared_seq;   // positions [0, shared_len) are read through sequence shared_seq
+  int32_t max_keys;            // bound on key_lens
+  float scale_log2;            // softmax scale * log2(e)
+  void* out;                   // [T, H, 512] bf16
+  float* lse;                  // [T, H] or nullptr
+  float* part_o;               // [slots, T * H, 512] (slots > 1)
+  float* part_lse;             // [slots, T * H]: base-2 log of each part's sum
+  int* err;
+};
+// keys: own_keys bounds the keys of each token's own part
+AttnPlan plan_attention(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, int sms);
+size_t attention_workspace(const AttnPlan& p, int64_t T, int32_t H);
+// returns the number of kernels launched through *launched
+cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, int* launched, cudaStream_t stream);
 
 int num_sms(int device);
 
