@@ -5,7 +5,7 @@
 // in one pass over the keys with a running maximum m.  Keys are cut into chunks; a row's parts (one per
 // chunk, each with its own m and sum) are joined by the second kernel.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 
@@ -16,7 +16,6 @@ namespace dsa {
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Cache row of position p of sequence seq, or -1 (reported) where the page table has no page for it.
@@ -52,18 +51,105 @@ __device__ __forceinline__ int32_t token_limit(const AttnArgs& a, int32_t t, int
   return n;
 }
 
-// One warp per row at a time: the plain form of the pass, no tiles.
-__global__ void __launch_bounds__(kThreads) attention_kernel(AttnArgs a, AttnPlan p) {
+// ------------------------------------------------------------------------------------------------ the pass
+
+// Shared memory of a CTA: operand blocks of 64 rows x 64 values (128-byte rows, 128-byte swizzle).
+constexpr uint32_t kBlock = 64 * 128;
+constexpr int kBlocks = (kLatentDim + kLatentRope) / 64;     // 8 blocks of latents, then the rotated part
+constexpr uint32_t kStage = kBlocks * kBlock;
+constexpr int kStages = 2;
+constexpr uint32_t kOffQ = 0;
+constexpr uint32_t kOffK = kStage;
+constexpr uint32_t kOffP = kOffK + kStages * kStage;
+constexpr uint32_t kSmemBytes = kOffP + kBlock + 1024;       // 1024: the blocks' alignment
+
+// Tensor memory columns: the output's 512 columns as two accumulators of 256 (a 64-row accumulator fills
+// 16 of every 32 lanes: the values 0 .. 255 in the lower, 256 .. 511 in the upper 16), two score tiles.
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemO = 0;
+constexpr uint32_t kTmemS = 256;
+constexpr uint32_t kUpperLanes = 16u << 16;
+
+constexpr int kSoftmaxWarps = 4;
+constexpr int kMmaWarp = 4;
+constexpr int kLoadWarps = 8;
+constexpr int kThreads = (kSoftmaxWarps + 1 + kLoadWarps) * 32;
+
+// The running maximum may lag behind the true one by this much (base 2) before the sums are rescaled:
+// fp32 sums and bf16 weights lose nothing by weights of up to 2^8.
+constexpr float kLag = 8.0f;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two E4M3 codes (the low 16 bits) times a power of two, exact in bf16.
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes, float scale) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(h) : "r"(codes));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return bf16x2(f.x * scale, f.y * scale);
+}
+
+struct __align__(8) Shared {
+  uint64_t full[kStages];       // a tile's keys are in shared memory
+  uint64_t empty[kStages];      // the tile's second product is done
+  uint64_t scores[2];           // a score tile is complete
+  uint64_t weights;             // the weights of a tile are in shared memory, the output is rescaled
+  uint64_t drained;             // every product of the CTA is done
+  uint32_t tmem;
+  int abort;
+  int32_t key_end;
+  int32_t limit[kAttnRows];     // keys at or past a row's limit are not its own
+  alignas(8) uint8_t valid[kStages][kLoadWarps];   // keys of a tile that exist, one bit each
+};
+
+// One CTA per work item: 64 rows against the keys [k0, key_end) in tiles of 64.
+//   8 warps bring each key's row into shared memory (gathered by 16-byte copies; FP8 rows are expanded to
+//   bf16 on the way), one thread issues the products S = Q K^T (64 x 64 x 576) and O += P V (64 x 512 x 64;
+//   V is the same tile read with its values contiguous), 4 warps turn S into weights P.
+// The product of tile i + 1 is issued before the second one of tile i, so the tensor cores work
+// while the weights of tile i are made.
+template <bool FP8>
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, AttnPlan p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  if (warp == kMmaWarp) {
+    if (lane == 0) {
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(&sh.full[i], kLoadWarps);
+        mbar_init(&sh.empty[i], 1);
+        mbar_init(&sh.scores[i], 1);
+      }
+      mbar_init(&sh.weights, kSoftmaxWarps);
+      mbar_init(&sh.drained, 1);
+      sh.abort = 0;
+      fence_barrier_init();
+    }
+    __syncwarp();
+    tmem_alloc(&sh.tmem, kTmemCols);
+    tmem_relinquish();
+  }
   grid_dependency_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+  // the item
   const int n_shared = p.shared_groups * p.shared_slots;
   int item = blockIdx.x;
-  int64_t row0, rows;
-  int slot, token = -1;
+  int64_t row0;                  // first of the item's rows in the packed [T, H]
+  int rows, slot, token = -1;
   int32_t k0, k1;
   if (item < n_shared) {
     row0 = static_cast<int64_t>(item % p.shared_groups) * kAttnRows;
-    rows = min(static_cast<int64_t>(kAttnRows), static_cast<int64_t>(a.T) * a.H - row0);
+    rows = static_cast<int>(min(static_cast<int64_t>(kAttnRows), static_cast<int64_t>(a.T) * a.H - row0));
     slot = item / p.shared_groups;
     k0 = slot * p.shared_chunk;
     k1 = min(k0 + p.shared_chunk, a.shared_len);
@@ -74,70 +160,366 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(AttnArgs a, AttnPla
     token = item % a.T;
     row0 = static_cast<int64_t>(token) * a.H + g * kAttnRows;
     rows = min(kAttnRows, a.H - g * kAttnRows);
-    const int own_slot = item / a.T;
-    slot = p.shared_slots + own_slot;
-    const int32_t base = a.idx ? 0 : a.shared_len;
-    k0 = base + own_slot * p.own_chunk;
+    slot = item / a.T;
+    k0 = (a.idx ? 0 : a.shared_len) + slot * p.own_chunk;
     k1 = min(k0 + p.own_chunk, a.idx ? a.top_k : a.max_keys);
+    slot += p.shared_slots;
   }
-  for (int64_t i = warp; i < rows; i += kThreads / 32) {
-    const int64_t r = row0 + i;
-    const int32_t t = static_cast<int32_t>(r / a.H), h = static_cast<int32_t>(r % a.H);
-    const int32_t seq = token_seq(a, t);
-    const int32_t limit = a.idx ? (seq < 0 ? 0 : a.top_k) : token_limit(a, t, seq);
-    const int32_t end = min(k1, limit);
-    const __nv_bfloat16* ql = static_cast<const __nv_bfloat16*>(a.q_latent) + t * a.ql_t + h * a.ql_h + lane * 16;
-    float q[16], o[16], q0 = 0.f, q1 = 0.f;
-    for (int e = 0; e < 16; ++e) {
-      q[e] = __bfloat162float(ql[e]);
-      o[e] = 0.f;
-    }
-    if (a.kv.rope) {
-      const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(a.q_rope) + t * a.qr_t + h * a.qr_h + lane * 2;
-      q0 = __bfloat162float(qr[0]);
-      q1 = __bfloat162float(qr[1]);
-    }
-    float m = -INFINITY, l = 0.f;
-    for (int32_t k = k0; k < end; ++k) {
-      const int32_t pos = a.idx ? a.idx[static_cast<int64_t>(t) * a.top_k + k] : k;
-      if (pos < 0) continue;
-      const int64_t row = cache_row(a.kv, token < 0 ? a.shared_seq : seq, pos, a.err, t);
-      if (row < 0) continue;
-      float c[16], s = 0.f;
-      for (int e = 0; e < 16; ++e) {
-        const int64_t at = row * kLatentDim + lane * 16 + e;
-        if (a.kv.fp8) {
-          __nv_fp8_e4m3 f;
-          f.__x = static_cast<const uint8_t*>(a.kv.latent)[at];
-          c[e] = static_cast<float>(f) * a.kv.scale[row];
-        } else {
-          c[e] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.kv.latent)[at]);
-        }
-        s += q[e] * c[e];
+  if (tid == 0) sh.key_end = 0;
+  __syncthreads();
+  int32_t seq = a.shared_seq;
+  if (token < 0) {
+    if (tid < kAttnRows) {
+      int32_t n = 0;
+      if (tid < rows) {
+        const int32_t t = static_cast<int32_t>((row0 + tid) / a.H);
+        n = token_limit(a, t, token_seq(a, t));
       }
-      if (a.kv.rope) {
-        const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(a.kv.rope) + row * kLatentRope + lane * 2;
-        s += q0 * __bfloat162float(kr[0]) + q1 * __bfloat162float(kr[1]);
-      }
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      s *= a.scale_log2;
-      const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn;
-      const float f = exp2f(m - ref), w = exp2f(s - ref);
-      l = l * f + w;
-      for (int e = 0; e < 16; ++e) o[e] = o[e] * f + w * c[e];
-      m = mn;
+      sh.limit[tid] = n;
+      atomicMax(&sh.key_end, min(n, k1));
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
-    if (p.slots() == 1) {
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + r * kLatentDim + lane * 16;
-      for (int e = 0; e < 16; ++e) out[e] = __float2bfloat16_rn(o[e] * inv);
-      if (a.lse && lane == 0) a.lse[r] = lse2 * kLn2;
+  } else {
+    seq = token_seq(a, token);
+    if (a.idx == nullptr) {
+      const int32_t n = token_limit(a, token, seq);
+      if (tid < kAttnRows) sh.limit[tid] = n;
+      if (tid == 0) sh.key_end = min(n, k1);
     } else {
-      const int64_t pr = static_cast<int64_t>(slot) * a.T * a.H + r;
-      for (int e = 0; e < 16; ++e) a.part_o[pr * kLatentDim + lane * 16 + e] = o[e] * inv;
-      if (lane == 0) a.part_lse[pr] = lse2;
+      // entries behind the last valid one (short histories are padded) are not visited
+      if (tid < kAttnRows) sh.limit[tid] = 0x7FFFFFFF;
+      int32_t last = 0;
+      if (seq >= 0)
+        for (int32_t k = k0 + tid; k < k1; k += kThreads)
+          if (a.idx[static_cast<int64_t>(token) * a.top_k + k] >= 0) last = k + 1;
+      last = __reduce_max_sync(0xffffffffu, last);
+      if (lane == 0) atomicMax(&sh.key_end, last);
     }
+  }
+  __syncthreads();
+  const int32_t key_end = sh.key_end;
+  const int tiles = key_end > k0 ? (key_end - k0 + kAttnTile - 1) / kAttnTile : 0;
+  const int blocks = a.kv.rope ? kBlocks : kBlocks - 1;
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  if (warp >= kMmaWarp + 1) {
+    // ---------------------------------------------------------------- loads
+    const int lw = warp - kMmaWarp - 1;                  // rows 8 lw .. 8 lw + 7 of every block
+    const int sub = lane >> 3, col = lane & 7;           // a lane's 16-byte column, rows sub and sub + 4
+    if (tiles > 0) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = lw * 8 + sub + 4 * j;
+        const bool ok = r < rows;
+        const int64_t qr = row0 + (ok ? r : 0);
+        const int64_t t = qr / a.H, h = qr % a.H;
+        const __nv_bfloat16* ql = static_cast<const __nv_bfloat16*>(a.q_latent) + t * a.ql_t + h * a.ql_h + col * 8;
+        const uint32_t dst = smem + kOffQ + r * 128 + ((col ^ (r & 7)) << 4);
+#pragma unroll
+        for (int c = 0; c < kBlocks - 1; ++c) cp_async16(dst + c * kBlock, ql + c * 64, ok);
+        if (blocks == kBlocks) {
+          const __nv_bfloat16* qx = static_cast<const __nv_bfloat16*>(a.q_rope) + t * a.qr_t + h * a.qr_h + col * 8;
+          cp_async16(dst + (kBlocks - 1) * kBlock, qx, ok);
+        }
+      }
+    }
+    int landed = 0, issued = 0;                          // tiles handed to the products, tiles under way
+    auto hand_over = [&](int i) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.full[i % kStages]);
+    };
+    for (int i = 0; i < tiles; ++i) {
+      const int st = i % kStages;
+      // the cache rows of this warp's 8 keys, one per lane (all lanes hold one of them)
+      const int32_t k = k0 + i * kAttnTile + lw * 8 + col;
+      int32_t pos = -1;
+      if (k < key_end) pos = a.idx ? a.idx[static_cast<int64_t>(token) * a.top_k + k] : k;
+      int64_t row = -1;
+      if (pos >= 0) row = cache_row(a.kv, seq, pos, a.err, token < 0 ? static_cast<int>(row0 / a.H) : token);
+      const uint32_t valid = __ballot_sync(0xffffffffu, row >= 0) & 0xFFu;
+      uint4 codes[8];
+      float scale = 0.f;
+      if constexpr (FP8) {
+        if (row >= 0) scale = a.kv.scale[row];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int64_t rj = __shfl_sync(0xffffffffu, row, j);
+          codes[j] = make_uint4(0u, 0u, 0u, 0u);
+          if (rj >= 0) codes[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.kv.latent) + rj * kLatentDim) + lane);
+        }
+      }
+      if (i >= kStages) {
+        for (; landed < i; ++landed) {                    // nothing may wait behind this wait
+          cp_async_wait<0>();
+          hand_over(landed);
+        }
+        const bool free_again = mbar_wait<true>(&sh.empty[st], ((i / kStages) - 1) & 1, &sh.abort);
+        if (!__all_sync(0xffffffffu, free_again)) break;  // a warp leaves as one
+      }
+      if (lane == 0) sh.valid[st][lw] = static_cast<uint8_t>(valid);
+      const uint32_t stage = smem + kOffK + st * kStage;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r8 = sub + 4 * j;
+        const int64_t rj = __shfl_sync(0xffffffffu, row, r8);
+        const bool ok = rj >= 0;
+        const int64_t at = ok ? rj : 0;
+        const uint32_t dst = stage + (lw * 8 + r8) * 128 + ((col ^ r8) << 4);
+        if constexpr (!FP8) {
+          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.kv.latent) + at * kLatentDim + col * 8;
+#pragma unroll
+          for (int c = 0; c < kBlocks - 1; ++c) cp_async16(dst + c * kBlock, src + c * 64, ok);
+        }
+        if (blocks == kBlocks)
+          cp_async16(dst + (kBlocks - 1) * kBlock, static_cast<const __nv_bfloat16*>(a.kv.rope) + at * kLatentRope + col * 8, ok);
+      }
+      cp_async_commit();
+      if constexpr (FP8) {
+        // lane l holds values 16 l .. 16 l + 15 of a row: two 16-byte columns of block l / 4.  Lanes of odd blocks
+        // store the second one first, so that the eight lanes of a store's phase fall on different banks.
+        const int swap = (lane >> 2) & 1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float s = __shfl_sync(0xffffffffu, scale, j);
+          const uint32_t w[4] = {codes[j].x, codes[j].y, codes[j].z, codes[j].w};
+          uint32_t v[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[2 * e] = e4m3x2_to_bf16x2(w[e] & 0xFFFFu, s);
+            v[2 * e + 1] = e4m3x2_to_bf16x2(w[e] >> 16, s);
+          }
+          const uint32_t base = stage + (lane >> 2) * kBlock + (lw * 8 + j) * 128;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int half = x ^ swap;
+            const uint32_t dst = base + ((((lane & 3) * 2 + half) ^ j) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(half ? v[4] : v[0]), "r"(half ? v[5] : v[1]),
+                         "r"(half ? v[6] : v[2]), "r"(half ? v[7] : v[3])
+                         : "memory");
+          }
+        }
+      }
+      ++issued;
+      if (i == 1) {                                       // the first tile need not wait for the second
+        cp_async_wait<1>();
+        hand_over(0);
+        landed = 1;
+      }
+    }
+    cp_async_wait<0>();
+    if (issued == tiles)
+      for (; landed < tiles; ++landed) hand_over(landed);
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------------- products
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = make_idesc(1, kAttnRows, kAttnTile);
+      constexpr uint32_t idesc_o = make_idesc(1, kAttnRows, 256) | kIdescBMnMajor;
+      bool ok = true;
+      auto second = [&](int i) {
+        if (!mbar_wait(&sh.weights, i & 1, &sh.abort)) return false;
+        tc_fence_after();
+        const uint32_t stage = smem + kOffK + (i % kStages) * kStage;
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+          for (int ks = 0; ks < kAttnTile / 16; ++ks)
+            umma_f16(tmem + kTmemO + half * kUpperLanes, sdesc_kmajor_sw128(smem + kOffP + ks * 32),
+                     sdesc_mnmajor_sw128(stage + half * 4 * kBlock + ks * 2048, kBlock), idesc_o, i > 0 || ks > 0);
+        umma_commit(&sh.empty[i % kStages]);
+        return true;
+      };
+      for (int i = 0; i < tiles && ok; ++i) {
+        ok = mbar_wait(&sh.full[i % kStages], (i / kStages) & 1, &sh.abort);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t stage = smem + kOffK + (i % kStages) * kStage;
+        const uint32_t d = tmem + kTmemS + (i & 1) * kAttnTile;
+        for (int c = 0; c < blocks; ++c)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_f16(d, sdesc_kmajor_sw128(smem + kOffQ + c * kBlock + ks * 32),
+                     sdesc_kmajor_sw128(stage + c * kBlock + ks * 32), idesc_s, c > 0 || ks > 0);
+        umma_commit(&sh.scores[i & 1]);
+        if (i > 0) ok = second(i - 1);
+      }
+      if (ok && tiles > 0) ok = second(tiles - 1);
+      umma_commit(&sh.drained);
+      int alone = 0;                                     // also after an abort: nothing may run on freed tensor memory
+      mbar_wait(&sh.drained, 0, &alone);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- weights
+    // The thread's two rows of the score tile: lane / 4 and lane / 4 + 8 of the warp's 16, 16 columns of each.
+    const int fr = lane >> 2;
+    const int32_t limit[2] = {sh.limit[warp * 16 + fr], sh.limit[warp * 16 + fr + 8]};
+    const uint32_t quadrant = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    bool ok = true;
+    for (int i = 0; i < tiles; ++i) {
+      ok = mbar_wait<true>(&sh.scores[i & 1], (i >> 1) & 1, &sh.abort);
+      ok = ok && mbar_wait<true>(&sh.full[i % kStages], (i / kStages) & 1, &sh.abort);   // for `valid`
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t raw[32];
+      tmem_ld_16x256b_x8(quadrant + kTmemS + (i & 1) * kAttnTile, raw);
+      const uint64_t present = *reinterpret_cast<const uint64_t*>(sh.valid[i % kStages]);
+      tmem_ld_wait();
+      float x[2][16];
+      const int32_t kb = k0 + i * kAttnTile;
+      uint64_t mask[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int32_t n = limit[r] - kb;                 // the row's keys of this tile
+        mask[r] = n >= kAttnTile ? present : n <= 0 ? 0ull : present & ((1ull << n) - 1);
+      }
+      const bool whole = __all_sync(0xffffffffu, (mask[0] & mask[1]) == ~0ull);
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) x[r][2 * j + e] = __uint_as_float(raw[4 * j + 2 * r + e]) * a.scale_log2;
+      if (!whole) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const uint64_t mine = mask[r] >> (2 * (lane & 3));
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!((mine >> (8 * j + e)) & 1)) x[r][2 * j + e] = -INFINITY;
+        }
+      }
+      float mx[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        mx[r] = x[r][0];
+#pragma unroll
+        for (int e = 1; e < 16; ++e) mx[r] = fmaxf(mx[r], x[r][e]);
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+      }
+      const bool rescale = __any_sync(0xffffffffu, mx[0] > m[0] + kLag || mx[1] > m[1] + kLag);
+      float factor[2] = {1.f, 1.f};
+      if (rescale) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float mn = fmaxf(m[r], mx[r]);
+          factor[r] = mn == -INFINITY ? 1.f : exp2_fast(m[r] - mn);
+          l[r] *= factor[r];
+          m[r] = mn;
+        }
+      }
+      uint32_t w[2][8];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float ref = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float lo = exp2_fast(x[r][2 * j] - ref), hi = exp2_fast(x[r][2 * j + 1] - ref);
+          l[r] += lo + hi;
+          w[r][j] = bf16x2(lo, hi);                      // the sum keeps fp32; the product's operand is bf16
+        }
+      }
+      if (i > 0) {                                       // the weights' buffer and the output are free again
+        ok = mbar_wait<true>(&sh.empty[(i - 1) % kStages], ((i - 1) / kStages) & 1, &sh.abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (rescale) {
+          tc_fence_after();
+          // an output lane's row is lane % 16: its factor sits with the lanes 4 (row % 8) of the score layout
+          const float f0 = __shfl_sync(0xffffffffu, factor[0], (lane & 7) * 4);
+          const float f1 = __shfl_sync(0xffffffffu, factor[1], (lane & 7) * 4);
+          const float f = lane & 8 ? f1 : f0;
+#pragma unroll 1
+          for (int c = 0; c < 256; c += 32) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(quadrant + kTmemO + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st_32x32b_x32(quadrant + kTmemO + c, o);
+          }
+          tmem_st_wait();
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint32_t dst = smem + kOffP + (warp * 16 + fr + 8 * r) * 128 + (lane & 3) * 4;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + ((j ^ fr) << 4)), "r"(w[r][j]) : "memory");
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.weights);
+    }
+    launch_dependents();
+    // ---------------------------------------------------------------- the result
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    }
+    // from the score layout to the output's: lane -> row lane % 16, values 256 (lane / 16) ..
+    const int src = (lane & 7) * 4;
+    const float l0 = __shfl_sync(0xffffffffu, l[0], src), l1 = __shfl_sync(0xffffffffu, l[1], src);
+    const float m0 = __shfl_sync(0xffffffffu, m[0], src), m1 = __shfl_sync(0xffffffffu, m[1], src);
+    const float sum = lane & 8 ? l1 : l0, top = lane & 8 ? m1 : m0;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
+    const int r = warp * 16 + (lane & 15);
+    const bool mine = r < rows;
+    const int64_t R = static_cast<int64_t>(a.T) * a.H;
+    const int64_t orow = p.slots() == 1 ? row0 + r : slot * R + row0 + r;
+    if (tiles > 0 && ok) {
+      ok = mbar_wait<true>(&sh.empty[(tiles - 1) % kStages], ((tiles - 1) / kStages) & 1, &sh.abort);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    }
+    if (ok && mine && lane < 16) {
+      if (p.slots() > 1) a.part_lse[orow] = lse2;
+      else if (a.lse) a.lse[orow] = lse2 * kLn2;
+    }
+    if (ok && (tiles > 0 || p.slots() == 1)) {
+#pragma unroll 1
+      for (int c = 0; c < 256; c += 32) {
+        uint32_t o[32];
+        if (tiles > 0) {
+          tmem_ld_32x32b_x32(quadrant + kTmemO + c, o);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        if (!mine) continue;
+        const int64_t at = orow * kLatentDim + (lane >> 4) * 256 + c;
+        // a row without keys is zero whatever its weights' products with foreign keys left
+        auto val = [&](int e) { return sum == 0.f ? 0.f : __uint_as_float(o[e]) * inv; };
+        if (p.slots() == 1) {
+          uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            out[e] = make_uint4(bf16x2(val(8 * e), val(8 * e + 1)), bf16x2(val(8 * e + 2), val(8 * e + 3)),
+                                bf16x2(val(8 * e + 4), val(8 * e + 5)), bf16x2(val(8 * e + 6), val(8 * e + 7)));
+        } else {
+          float4* out = reinterpret_cast<float4*>(a.part_o + at);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) out[e] = make_float4(val(4 * e), val(4 * e + 1), val(4 * e + 2), val(4 * e + 3));
+        }
+      }
+    }
+  }
+  if (sh.abort && lane == 0) record_error(a.err, DSA_DEVERR_TIMEOUT, static_cast<int>(blockIdx.x));
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
   }
 }
 
@@ -209,12 +591,17 @@ cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, int* launched
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(int64_t(p.shared_groups) * p.shared_slots + int64_t(a.T) * p.own_groups * p.own_slots));
   cfg.blockDim = dim3(kThreads);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, attention_kernel, a, p);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  auto kernel = a.kv.fp8 ? attention_kernel<true> : attention_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  e = cudaLaunchKernelEx(&cfg, kernel, a, p);
   if (e != cudaSuccess) return e;
   ++*launched;
   if (p.slots() > 1) {
     cfg.gridDim = dim3(static_cast<unsigned>(int64_t(a.T) * a.H));
     cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, attention_join_kernel, a, static_cast<int>(p.slots()));
     if (e != cudaSuccess) return e;
     ++*launched;
