@@ -384,41 +384,55 @@ class LatentCache:
         return self.latent.dtype in (torch.uint8, torch.float8_e4m3fn)
 
     def c(self) -> _lib.LatentCacheView:
-        _require_cuda(self.latent, self.rope, self.scale)
-        rows = self.latent.shape[0]
-        if self.page_size < 1 or rows % self.page_size:
+        latent, rope, scale, page_size = self.latent, self.rope, self.scale, self.page_size
+        rows, d_c = latent.shape
+        fp8 = latent.dtype is not torch.bfloat16
+        if page_size < 1 or rows % page_size:
             raise ValueError("the cache must hold whole pages")
-        if not self.fp8 and self.latent.dtype != torch.bfloat16:
-            raise TypeError("latent must be bf16 or uint8 (E4M3 codes)")
-        if self.rope is not None and (self.rope.dtype != torch.bfloat16 or self.rope.shape[0] != rows):
+        if fp8:
+            if not self.fp8:
+                raise TypeError("latent must be bf16 or uint8 (E4M3 codes)")
+            if scale is None or scale.dtype is not torch.float32 or scale.numel() != rows:
+                raise ValueError("an FP8 latent cache needs one fp32 scale per row")
+        if rope is not None and (rope.dtype is not torch.bfloat16 or rope.shape[0] != rows):
             raise ValueError("rope must be bf16 with a row for each latent row")
-        if self.fp8 and (self.scale is None or self.scale.dtype != torch.float32 or self.scale.numel() != rows):
-            raise ValueError("an FP8 latent cache needs one fp32 scale per row")
-        return _lib.LatentCacheView(self.latent.data_ptr(), self.scale.data_ptr() if self.scale is not None else None,
-                                    self.rope.data_ptr() if self.rope is not None else None, rows // self.page_size,
-                                    self.page_size, self.latent.shape[1], 0 if self.rope is None else self.rope.shape[1],
-                                    DSA_FP8_E4M3 if self.fp8 else DSA_BF16)
+        return _lib.LatentCacheView(latent.data_ptr(), scale.data_ptr() if fp8 else None,
+                                    None if rope is None else rope.data_ptr(), rows // page_size, page_size, d_c,
+                                    0 if rope is None else rope.shape[1], DSA_FP8_E4M3 if fp8 else DSA_BF16)
 
 
-def _on(first: torch.Tensor, stream, *others):
-    """(device guard, stream guard, stream): the calls below run on their tensors' device, and what they
-    allocate belongs to the stream that they launch on."""
-    for t in (first,) + others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}: one device is wanted")
-    if first.device.type != "cuda":
+# The calls below are short on the GPU, so the path to them is too: on the current device and its current
+# stream they go straight to the library; otherwise they call themselves again inside the guards.
+
+def _elsewhere(t, stream):
+    """The guard under which a call on t's device and `stream` belongs, or None where it is current already."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("device tensors must be CUDA tensors")
     if stream is None:
-        stream = torch.cuda.current_stream(first.device)
-    elif stream.device != first.device:
-        raise ValueError(f"stream on {stream.device}, tensors on {first.device}")
-    return torch.cuda.stream(stream), ctypes.c_void_p(stream.cuda_stream)
+        return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"stream on {stream.device}, tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def _raw_stream(t):
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _one_device(first, *ts, contiguous=True):
+    dev = first.get_device()
+    for t in ts:
+        if t is not None and (t.get_device() != dev or (contiguous and not t.is_contiguous())):
+            if t.get_device() != dev:
+                raise ValueError(f"tensors on {first.device} and {t.device}: one device is wanted")
+            raise ValueError("device tensors must be contiguous CUDA tensors")
 
 
 def _int32(name, t, *shape):
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise TypeError(f"{name} must be int32")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
 
@@ -433,36 +447,45 @@ def dsa_rmsnorm_fp8(x, weight, eps=1e-6, residual=None, group=128, residual_out=
     rows, d = x.shape
     if weight.numel() != d:
         raise ValueError("weight must hold d values")
-    if group not in (0, 128):
+    if group != 128 and group != 0:
         raise ValueError("group must be 0 (one scale per row) or 128")
-    guard, st = _on(x, stream, weight, residual, residual_out, codes, scale, normed)
-    with guard:
-        if residual is not None and residual_out is None:
-            residual_out = torch.empty(rows, d, dtype=residual.dtype, device=x.device)
-        if codes is None:
-            codes = torch.empty(rows, d, dtype=torch.uint8, device=x.device)
-        if scale is None:
-            scale = torch.empty(rows, -(-d // 128) if group else 1, dtype=torch.float32, device=x.device)
-        _require_cuda(weight, residual, residual_out, codes, scale, normed)
-        for name, t, dt, n in (("residual", residual, (x.dtype,), rows * d), ("residual_out", residual_out, (x.dtype,), rows * d),
-                               ("codes", codes, (torch.uint8, torch.float8_e4m3fn), rows * d),
-                               ("scale", scale, (torch.float32,), rows * (-(-d // 128) if group else 1)),
-                               ("normed", normed, (torch.bfloat16,), rows * d)):
-            if t is not None and t.dtype not in dt:
-                raise TypeError(f"{name} must be {dt[0]}")
-            if t is not None and t.numel() != n:
-                raise ValueError(f"{name} must hold {n} values")
-        check(_lib.load().dsa_rmsnorm_fp8(_ptr(x), _dtype_code(x), x.stride(0), _ptr(residual), _ptr(residual_out),
-                                          _ptr(weight), _dtype_code(weight), rows, d, float(eps), int(group),
-                                          _ptr(codes), _ptr(scale), _ptr(normed), st))
+    guard = _elsewhere(x, stream)
+    if guard is not None:
+        with guard:
+            return dsa_rmsnorm_fp8(x, weight, eps, residual, group, residual_out, codes, scale, normed)
+    n, groups = rows * d, -(-d // 128) if group else 1
+    if residual is not None:
+        if residual.dtype is not x.dtype or residual.numel() != n:
+            raise ValueError(f"residual must hold {n} values of {x.dtype}")
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+        elif residual_out.dtype is not x.dtype or residual_out.numel() != n:
+            raise ValueError(f"residual_out must hold {n} values of {x.dtype}")
+    if codes is None:
+        codes = torch.empty((rows, d), dtype=torch.uint8, device=x.device)
+    elif codes.element_size() != 1 or codes.numel() != n:
+        raise ValueError(f"codes must hold {n} bytes")
+    if scale is None:
+        scale = torch.empty((rows, groups), dtype=torch.float32, device=x.device)
+    elif scale.dtype is not torch.float32 or scale.numel() != rows * groups:
+        raise ValueError(f"scale must hold {rows * groups} fp32 values")
+    if normed is not None and (normed.dtype is not torch.bfloat16 or normed.numel() != n):
+        raise ValueError(f"normed must hold {n} bf16 values")
+    _one_device(x, weight, residual, residual_out, codes, scale, normed)
+    check(_lib.load().dsa_rmsnorm_fp8(x.data_ptr(), _dtype_code(x), x.stride(0), _address(residual), _address(residual_out),
+                                      weight.data_ptr(), _dtype_code(weight), rows, d, eps, group, codes.data_ptr(),
+                                      scale.data_ptr(), _address(normed), _raw_stream(x)))
     return codes, scale, residual_out
 
 
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
 def _page_table(page_table) -> _lib.PageTable:
-    if page_table.dim() != 2 or page_table.dtype != torch.int32:
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2:
         raise TypeError("page_table must be int32 [num_seqs, max_pages]")
-    _require_cuda(page_table)
-    return _lib.PageTable(page_table.data_ptr(), page_table.shape[0], page_table.shape[1])
+    return _lib.PageTable(page_table.data_ptr(), *page_table.shape)
 
 
 def dsa_latent_append_rope(cache: LatentCache, page_table, c_new, kr_new, seq_ids, positions, rope_dim=None,
@@ -471,58 +494,67 @@ def dsa_latent_append_rope(cache: LatentCache, page_table, c_new, kr_new, seq_id
     (bf16 / fp32, rows may be strided; None for a cache without a rotated part) of positions ``positions`` (int32 [n]) of
     sequences ``seq_ids`` (int32 [n], negative: a padding token).  ``page_table`` int32 [num_seqs, max_pages]."""
     n = c_new.shape[0]
-    for name, t, width in (("c_new", c_new, 512), ("kr_new", kr_new, 64)):
-        if t is None and name == "kr_new" and cache.rope is None:
-            continue
-        if t is None or t.dim() != 2 or t.shape[0] != n or t.shape[1] != width or (n and t.stride(1) != 1):
-            raise ValueError(f"{name} must be [n, {width}] with contiguous rows")
-    if kr_new is not None and kr_new.dtype != c_new.dtype:
-        raise TypeError("c_new and kr_new must have one dtype")
+    if c_new.shape != (n, 512) or (n and c_new.stride(1) != 1):
+        raise ValueError("c_new must be [n, 512] with contiguous rows")
+    kr_stride = 0
+    if cache.rope is not None:
+        if kr_new is None or kr_new.shape != (n, 64) or (n and kr_new.stride(1) != 1):
+            raise ValueError("kr_new must be [n, 64] with contiguous rows")
+        if kr_new.dtype is not c_new.dtype:
+            raise TypeError("c_new and kr_new must have one dtype")
+        kr_stride = kr_new.stride(0)
+    else:
+        kr_new = None
     _int32("seq_ids", seq_ids, n)
     _int32("positions", positions, n)
-    _require_cuda(seq_ids, positions)
-    guard, st = _on(cache.latent, stream, cache.rope, cache.scale, page_table, c_new, kr_new, seq_ids, positions)
-    cc, pt, r = cache.c(), _page_table(page_table), _rope(64, rope_dim, base, interleaved)
-    with guard:
-        check(_lib.load().dsa_latent_append_rope(ctypes.byref(cc), ctypes.byref(pt), _ptr(c_new), c_new.stride(0),
-                                                 _ptr(kr_new), 0 if kr_new is None else kr_new.stride(0),
-                                                 _dtype_code(c_new), _ptr(seq_ids), _ptr(positions), n, ctypes.byref(r),
-                                                 st))
+    guard = _elsewhere(cache.latent, stream)
+    if guard is not None:
+        with guard:
+            return dsa_latent_append_rope(cache, page_table, c_new, kr_new, seq_ids, positions, rope_dim, base, interleaved)
+    _one_device(cache.latent, cache.rope, cache.scale, cache.latent, page_table, seq_ids, positions)
+    _one_device(cache.latent, c_new, kr_new, contiguous=False)
+    check(_lib.load().dsa_latent_append_rope(cache.c(), _page_table(page_table), c_new.data_ptr(), c_new.stride(0),
+                                             _address(kr_new), kr_stride, _dtype_code(c_new), seq_ids.data_ptr(),
+                                             positions.data_ptr(), n, _rope(64, rope_dim, base, interleaved),
+                                             _raw_stream(c_new)))
 
 
-def _attend(call, q_latent, q_rope, cache, page_table, out, lse, stream, workspace, workspace_bytes, *ints):
-    for name, t, width in (("q_latent", q_latent, 512), ("q_rope", q_rope, 64)):
-        if t is None and name == "q_rope" and cache.rope is None:
-            continue
-        if t is None or t.dim() != 3 or t.shape[2] != width or t.shape[:2] != q_latent.shape[:2]:
-            raise ValueError(f"{name} must be [T, H, {width}]")
-        if t.dtype != torch.bfloat16:
-            raise TypeError(f"{name} must be bf16")
-        if t.numel() and t.stride(2) != 1:
-            raise ValueError(f"{name} must be contiguous in its last dimension")
+def _latent_query(q_latent, q_rope, cache) -> _lib.LatentQuery:
+    if q_latent.dim() != 3 or q_latent.shape[2] != 512:
+        raise ValueError("q_latent must be [T, H, 512]")
     T, H, _ = q_latent.shape
-    _require_cuda(*ints)
-    guard, st = _on(q_latent, stream, q_rope, cache.latent, cache.rope, cache.scale, page_table, out, lse, workspace, *ints)
-    cc, pt = cache.c(), _page_table(page_table)
-    qr = (0, 0, 0) if q_rope is None else (q_rope.data_ptr(), q_rope.stride(0), q_rope.stride(1))
-    qq = _lib.LatentQuery(q_latent.data_ptr(), q_latent.stride(0), q_latent.stride(1), *qr, T, H)
-    with guard:
-        if out is None:
-            out = torch.empty(T, H, 512, dtype=torch.bfloat16, device=q_latent.device)
-        if lse is None:
-            lse = torch.empty(T, H, dtype=torch.float32, device=q_latent.device)
-        _require_cuda(out, lse, workspace)
-        if out.dtype != torch.bfloat16 or lse.dtype != torch.float32:
-            raise TypeError("out must be bf16 and lse fp32")
-        if out.numel() != T * H * 512 or lse.numel() != T * H:
-            raise ValueError("out must be [T, H, 512] and lse [T, H]")
-        if workspace is None:
-            # from torch's allocator, so that a captured graph keeps its own
-            need = workspace_bytes(T, H)
-            workspace = torch.empty(need, dtype=torch.uint8, device=q_latent.device) if need else None
-        ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        check(call(ctypes.byref(qq), ctypes.byref(cc), ctypes.byref(pt), _ptr(out), _ptr(lse), _ptr(workspace), ws, st))
-    return out, lse
+    st, sh, one = q_latent.stride()
+    if q_latent.dtype is not torch.bfloat16:
+        raise TypeError("q_latent must be bf16")
+    if cache.rope is None:
+        if one != 1:
+            raise ValueError("q_latent must be contiguous in its last dimension")
+        return _lib.LatentQuery(q_latent.data_ptr(), st, sh, None, 0, 0, T, H)
+    if q_rope is None or q_rope.shape != (T, H, 64):
+        raise ValueError(f"q_rope must be [{T}, {H}, 64]")
+    if q_rope.dtype is not torch.bfloat16:
+        raise TypeError("q_rope must be bf16")
+    rt, rh, rone = q_rope.stride()
+    if one != 1 or rone != 1:
+        raise ValueError("q_latent and q_rope must be contiguous in their last dimension")
+    return _lib.LatentQuery(q_latent.data_ptr(), st, sh, q_rope.data_ptr(), rt, rh, T, H)
+
+
+def _outputs(T, H, q_latent, out, lse, workspace, need):
+    """(out, lse, workspace of `need` bytes); what is not given comes from torch's allocator, so that a captured
+    graph keeps its own."""
+    dev = q_latent.device
+    if out is None:
+        out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=dev)
+    elif out.dtype is not torch.bfloat16 or out.numel() != T * H * 512:
+        raise ValueError("out must hold [T, H, 512] bf16 values")
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    elif lse.dtype is not torch.float32 or lse.numel() != T * H:
+        raise ValueError("lse must hold [T, H] fp32 values")
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    return out, lse, workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
 def dsa_sparse_attention(q_latent, q_rope, cache: LatentCache, page_table, seq_ids, idx, sm_scale, out=None, lse=None,
@@ -531,18 +563,25 @@ def dsa_sparse_attention(q_latent, q_rope, cache: LatentCache, page_table, seq_i
     whole 16-byte vectors; q_rope None for a cache without a rotated part) of sequences ``seq_ids`` (int32 [T], negative:
     padding) over the positions ``idx`` (int32 [T, k], -1: no entry) of the paged cache.  Returns (out bf16
     [T, H, 512], lse fp32 [T, H]).  ``workspace``: uint8 of dsa_sparse_attention_workspace_bytes (default: allocated)."""
-    lib, T = _lib.load(), q_latent.shape[0]
+    q = _latent_query(q_latent, q_rope, cache)
+    T, H = q.T, q.H
     if idx.dim() != 2:
         raise ValueError("idx must be [T, k]")
-    _int32("seq_ids", seq_ids, T)
-    _int32("idx", idx, T, idx.shape[1])
     k = idx.shape[1]
-
-    def call(q, c, p, o, l, w, n, st):
-        return lib.dsa_sparse_attention(q, c, p, _ptr(seq_ids), _ptr(idx), k, float(sm_scale), o, l, w, n, st)
-
-    return _attend(call, q_latent, q_rope, cache, page_table, out, lse, stream, workspace,
-                   lambda t, h: lib.dsa_sparse_attention_workspace_bytes(t, h, k), seq_ids, idx)
+    _int32("seq_ids", seq_ids, T)
+    _int32("idx", idx, T, k)
+    guard = _elsewhere(q_latent, stream)
+    if guard is not None:
+        with guard:
+            return dsa_sparse_attention(q_latent, q_rope, cache, page_table, seq_ids, idx, sm_scale, out, lse, workspace)
+    lib = _lib.load()
+    need = lib.dsa_sparse_attention_workspace_bytes(T, H, k) if workspace is None else 0
+    out, lse, workspace, given = _outputs(T, H, q_latent, out, lse, workspace, need)
+    _one_device(q_latent, cache.latent, cache.rope, cache.scale, page_table, seq_ids, idx, out, lse, workspace)
+    _one_device(q_latent, q_rope, contiguous=False)
+    check(lib.dsa_sparse_attention(q, cache.c(), _page_table(page_table), seq_ids.data_ptr(), idx.data_ptr(), k, sm_scale,
+                                   out.data_ptr(), lse.data_ptr(), _address(workspace), given, _raw_stream(q_latent)))
+    return out, lse
 
 
 def dsa_prefix_attention(q_latent, q_rope, cache: LatentCache, page_table, seq_ids, key_lens, sm_scale, prefix_len=0,
@@ -550,18 +589,27 @@ def dsa_prefix_attention(q_latent, q_rope, cache: LatentCache, page_table, seq_i
     """Attention over every cached position below ``key_lens`` (int32 [T]), the first ``prefix_len`` shared by the whole
     batch and read once, through row ``prefix_seq`` of the page table.  ``max_keys`` bounds key_lens (default: what the
     page table can hold).  Other arguments and results as dsa_sparse_attention."""
-    lib, T = _lib.load(), q_latent.shape[0]
+    q = _latent_query(q_latent, q_rope, cache)
+    T, H = q.T, q.H
     _int32("seq_ids", seq_ids, T)
     _int32("key_lens", key_lens, T)
+    guard = _elsewhere(q_latent, stream)
+    if guard is not None:
+        with guard:
+            return dsa_prefix_attention(q_latent, q_rope, cache, page_table, seq_ids, key_lens, sm_scale, prefix_len,
+                                        prefix_seq, max_keys, out, lse, workspace)
+    table = _page_table(page_table)
     if max_keys is None:
-        max_keys = page_table.shape[1] * cache.page_size
-    m, p0, s0 = int(max_keys), int(prefix_len), int(prefix_seq)
-
-    def call(q, c, p, o, l, w, n, st):
-        return lib.dsa_prefix_attention(q, c, p, _ptr(seq_ids), _ptr(key_lens), p0, s0, m, float(sm_scale), o, l, w, n, st)
-
-    return _attend(call, q_latent, q_rope, cache, page_table, out, lse, stream, workspace,
-                   lambda t, h: lib.dsa_prefix_attention_workspace_bytes(t, h, p0, m), seq_ids, key_lens)
+        max_keys = table.max_pages * cache.page_size
+    lib = _lib.load()
+    need = lib.dsa_prefix_attention_workspace_bytes(T, H, prefix_len, max_keys) if workspace is None else 0
+    out, lse, workspace, given = _outputs(T, H, q_latent, out, lse, workspace, need)
+    _one_device(q_latent, cache.latent, cache.rope, cache.scale, page_table, seq_ids, key_lens, out, lse, workspace)
+    _one_device(q_latent, q_rope, contiguous=False)
+    check(lib.dsa_prefix_attention(q, cache.c(), table, seq_ids.data_ptr(), key_lens.data_ptr(), prefix_len, prefix_seq,
+                                   max_keys, sm_scale, out.data_ptr(), lse.data_ptr(), _address(workspace), given,
+                                   _raw_stream(q_latent)))
+    return out, lse
 
 
 def dsa_sparse_attention_workspace_bytes(T: int, H: int, top_k: int) -> int:

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -1329,9 +1330,13 @@ dsa_status_t check_latent_query(const dsa_latent_query_t* q, const LatentView& v
 }
 
 int current_sms() {
+  static std::atomic<int> known[64];                   // a device's count does not change
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
-  return num_sms(dev);
+  if (dev >= 64) return num_sms(dev);
+  int n = known[dev].load(std::memory_order_relaxed);
+  if (n == 0) known[dev].store(n = num_sms(dev), std::memory_order_relaxed);
+  return n;
 }
 
 // Workspace of one attention call: the caller's, or the stream's own.

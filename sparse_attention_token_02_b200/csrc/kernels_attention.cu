@@ -8,6 +8,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -552,27 +553,39 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
+// Cuts a call into items.  One size of chunk serves the shared and the own part.  An item costs its
+// tiles and about four tiles' time beside them (set-up, queries, result); splitting a row into parts costs
+// the join and the parts' traffic.  Candidates: no split, and the smallest chunks that fill 1 .. 4 waves.
 AttnPlan plan_attention(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, int sms) {
   const int64_t R = T * H, shared_tiles = ceil_div(shared_keys, kAttnTile);
   // a call with no keys at all still writes its empty rows
   const int64_t own_tiles = own_keys > 0 || shared_keys == 0 ? std::max<int64_t>(1, ceil_div(own_keys, kAttnTile)) : 0;
   const int64_t longest = std::max(shared_tiles, own_tiles);
+  const int64_t shared_groups = ceil_div(R, kAttnRows), own_groups = ceil_div(H, kAttnRows);
   AttnPlan best{};
   double best_cost = 0.0;
-  for (int64_t k = 1; k <= std::min<int64_t>(longest, 160); ++k) {
-    const int64_t chunk = ceil_div(longest, k);
+  auto consider = [&](int64_t chunk) {
     AttnPlan p{};
-    p.shared_groups = static_cast<int32_t>(ceil_div(R, kAttnRows));
-    p.own_groups = static_cast<int32_t>(ceil_div(H, kAttnRows));
+    p.shared_groups = static_cast<int32_t>(shared_groups);
+    p.own_groups = static_cast<int32_t>(own_groups);
     p.shared_slots = static_cast<int32_t>(ceil_div(shared_tiles, chunk));
     p.own_slots = static_cast<int32_t>(ceil_div(own_tiles, chunk));
-    p.shared_chunk = p.own_chunk = static_cast<int32_t>(std::min<int64_t>(chunk, longest) * kAttnTile);
-    const int64_t items = int64_t(p.shared_groups) * p.shared_slots + T * p.own_groups * p.own_slots;
-    const double cost = ceil_div(items, sms) * (chunk + 4.0) + (p.slots() > 1 ? 3.0 + p.slots() * R * 0.0006 : 0.0);
-    if (k == 1 || cost < best_cost) {
+    p.shared_chunk = p.own_chunk = static_cast<int32_t>(chunk * kAttnTile);
+    const int64_t items = shared_groups * p.shared_slots + T * own_groups * p.own_slots;
+    const double cost = ceil_div(items, sms) * (chunk + 4.0) + (p.slots() > 1 ? 3.0 + double(p.slots()) * R * 0.0006 : 0.0);
+    if (best.slots() == 0 || cost < best_cost) {
       best = p;
       best_cost = cost;
     }
+    return items;
+  };
+  consider(longest);
+  const int64_t tiles = shared_groups * shared_tiles + T * own_groups * own_tiles;
+  for (int waves = 1; waves <= 4; ++waves) {
+    const int64_t room = int64_t(waves) * sms;
+    int64_t chunk = std::min(longest, ceil_div(tiles, room));
+    // rounding up to whole chunks can need more items than fit: grow the chunk until they do
+    while (chunk < longest && consider(chunk) > room) chunk += std::max<int64_t>(1, chunk / 16);
   }
   return best;
 }
@@ -593,8 +606,17 @@ cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, int* launched
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   auto kernel = a.kv.fp8 ? attention_kernel<true> : attention_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  // once per device and kernel: the attribute stays with the device's context
+  static std::atomic<uint64_t> ready[2];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (!(ready[a.kv.fp8].load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    ready[a.kv.fp8].fetch_or(bit, std::memory_order_relaxed);
+  }
   e = cudaLaunchKernelEx(&cfg, kernel, a, p);
   if (e != cudaSuccess) return e;
   ++*launched;
