@@ -20,7 +20,7 @@ namespace {
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Cache row of position p of sequence seq, or -1 (reported) where the page table has no page for it.
-__device__ __forceinline__ int64_t cache_row(const LatentView& kv, int32_t seq, int32_t p, int* err, int info) {
+__device__ __forceinline__ int32_t cache_row(const LatentView& kv, int32_t seq, int32_t p, int* err, int info) {
   const int32_t slot = p / kv.page_size;
   int32_t page = -1;
   if (slot < kv.max_pages) page = kv.pages[static_cast<int64_t>(seq) * kv.max_pages + slot];
@@ -28,7 +28,7 @@ __device__ __forceinline__ int64_t cache_row(const LatentView& kv, int32_t seq, 
     record_error(err, DSA_DEVERR_PAGE, info);
     return -1;
   }
-  return static_cast<int64_t>(page) * kv.page_size + (p - slot * kv.page_size);
+  return page * kv.page_size + (p - slot * kv.page_size);      // fewer than 2^31 rows
 }
 
 // Sequence of token t: -1 for a padding token and (reported) for one outside the page table.
@@ -54,18 +54,24 @@ __device__ __forceinline__ int32_t token_limit(const AttnArgs& a, int32_t t, int
 
 // ------------------------------------------------------------------------------------------------ the pass
 
-// Shared memory of a CTA: operand blocks of 64 rows x 64 values (128-byte rows, 128-byte swizzle).
+// Shared memory of a CTA: operand blocks of 64 rows x 64 values (128-byte rows, 128-byte swizzle): the
+// queries, then two stages of keys.  A tile's weights take the place of its keys' rotated part, which
+// only the first product reads.
 constexpr uint32_t kBlock = 64 * 128;
-constexpr int kBlocks = (kLatentDim + kLatentRope) / 64;     // 8 blocks of latents, then the rotated part
-constexpr uint32_t kStage = kBlocks * kBlock;
+constexpr int kLatentBlocks = kLatentDim / 64;               // 8; the rotated part is a ninth
+constexpr int kHalf = kLatentBlocks / 2;                     // blocks per half: values 0 .. 255, 256 .. 511
+constexpr uint32_t kStage = (kLatentBlocks + 1) * kBlock;
+constexpr uint32_t kWeights = kLatentBlocks * kBlock;        // within a stage
 constexpr int kStages = 2;
-constexpr uint32_t kOffQ = 0;
 constexpr uint32_t kOffK = kStage;
-constexpr uint32_t kOffP = kOffK + kStages * kStage;
-constexpr uint32_t kSmemBytes = kOffP + kBlock + 1024;       // 1024: the blocks' alignment
+constexpr uint32_t kSmemBytes = kOffK + kStages * kStage + 1024;   // 1024: the blocks' alignment
+// the result on its way out, over the keys' stages: rows of 512 fp32 or bf16 values, padded to spread the banks
+constexpr uint32_t kOutRow32 = kLatentDim * 4 + 16, kOutRow16 = kLatentDim * 2 + 16;
+static_assert(64 * kOutRow32 <= kStages * kStage, "the result must fit");
 
 // Tensor memory columns: the output's 512 columns as two accumulators of 256 (a 64-row accumulator fills
 // 16 of every 32 lanes: the values 0 .. 255 in the lower, 256 .. 511 in the upper 16), two score tiles.
+// All 512 columns are taken, so the allocation starts at column 0, a constant for the issuing thread.
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 0;
 constexpr uint32_t kTmemS = 256;
@@ -100,10 +106,10 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes, float scale
 }
 
 struct __align__(8) Shared {
-  uint64_t full[kStages];       // a tile's keys are in shared memory
-  uint64_t empty[kStages];      // the tile's second product is done
+  uint64_t full[kStages][2];    // a half of a tile's keys is in shared memory (the second half with the rotated part)
+  uint64_t empty[kStages][2];   // a half of the tile's second product is done
   uint64_t scores[2];           // a score tile is complete
-  uint64_t weights;             // the weights of a tile are in shared memory, the output is rescaled
+  uint64_t weights[2];          // the weights of a tile are in shared memory, the output is rescaled
   uint64_t drained;             // every product of the CTA is done
   uint32_t tmem;
   int abort;
@@ -116,8 +122,9 @@ struct __align__(8) Shared {
 //   8 warps bring each key's row into shared memory (gathered by 16-byte copies; FP8 rows are expanded to
 //   bf16 on the way), one thread issues the products S = Q K^T (64 x 64 x 576) and O += P V (64 x 512 x 64;
 //   V is the same tile read with its values contiguous), 4 warps turn S into weights P.
-// The product of tile i + 1 is issued before the second one of tile i, so the tensor cores work
-// while the weights of tile i are made.
+// Products are issued in the order in which their operands come: the first of tile i + 1 runs while
+// the weights of tile i are made.  Tiles go in and out in halves of 256 values, so that the loads
+// of one half run under the products of the other.
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, AttnPlan p) {
   extern __shared__ uint8_t smem_raw[];
@@ -127,30 +134,34 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
   if (warp == kMmaWarp) {
     if (lane == 0) {
       for (int i = 0; i < kStages; ++i) {
-        mbar_init(&sh.full[i], kLoadWarps);
-        mbar_init(&sh.empty[i], 1);
+        for (int h = 0; h < 2; ++h) {
+          mbar_init(&sh.full[i][h], kLoadWarps);
+          mbar_init(&sh.empty[i][h], 1);
+        }
         mbar_init(&sh.scores[i], 1);
+        mbar_init(&sh.weights[i], kSoftmaxWarps);
       }
-      mbar_init(&sh.weights, kSoftmaxWarps);
       mbar_init(&sh.drained, 1);
       sh.abort = 0;
+      sh.key_end = 0;
       fence_barrier_init();
     }
     __syncwarp();
     tmem_alloc(&sh.tmem, kTmemCols);
     tmem_relinquish();
   }
+  __syncthreads();
   grid_dependency_wait();
 
   // the item
   const int n_shared = p.shared_groups * p.shared_slots;
   int item = blockIdx.x;
-  int64_t row0;                  // first of the item's rows in the packed [T, H]
+  int row0;                      // first of the item's rows in the packed [T, H]
   int rows, slot, token = -1;
   int32_t k0, k1;
   if (item < n_shared) {
-    row0 = static_cast<int64_t>(item % p.shared_groups) * kAttnRows;
-    rows = static_cast<int>(min(static_cast<int64_t>(kAttnRows), static_cast<int64_t>(a.T) * a.H - row0));
+    row0 = item % p.shared_groups * kAttnRows;
+    rows = min(kAttnRows, a.T * a.H - row0);
     slot = item / p.shared_groups;
     k0 = slot * p.shared_chunk;
     k1 = min(k0 + p.shared_chunk, a.shared_len);
@@ -159,21 +170,37 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
     const int g = item % p.own_groups;
     item /= p.own_groups;
     token = item % a.T;
-    row0 = static_cast<int64_t>(token) * a.H + g * kAttnRows;
+    row0 = token * a.H + g * kAttnRows;
     rows = min(kAttnRows, a.H - g * kAttnRows);
     slot = item / a.T;
     k0 = (a.idx ? 0 : a.shared_len) + slot * p.own_chunk;
     k1 = min(k0 + p.own_chunk, a.idx ? a.top_k : a.max_keys);
     slot += p.shared_slots;
   }
-  if (tid == 0) sh.key_end = 0;
-  __syncthreads();
+  const int32_t* idx = a.idx ? a.idx + static_cast<int64_t>(token) * a.top_k : nullptr;
+  const int lw = warp - kMmaWarp - 1;                    // loads: rows 8 lw .. 8 lw + 7 of every block
+  const int sub = lane >> 3, col = lane & 7;             // a lane's 16-byte column, rows sub and sub + 4
+  if (lw >= 0) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {                        // the queries; they arrive with the first tile's second half
+      const int r = lw * 8 + sub + 4 * j;
+      const bool ok = r < rows;
+      const int qr = row0 + (ok ? r : 0);
+      const int t = qr / a.H, h = qr - t * a.H;
+      const __nv_bfloat16* ql = static_cast<const __nv_bfloat16*>(a.q_latent) + t * a.ql_t + h * a.ql_h + col * 8;
+      const uint32_t dst = smem + r * 128 + ((col ^ (r & 7)) << 4);
+#pragma unroll
+      for (int c = 0; c < kLatentBlocks; ++c) cp_async16(dst + c * kBlock, ql + c * 64, ok);
+      if (a.kv.rope)
+        cp_async16(dst + kWeights, static_cast<const __nv_bfloat16*>(a.q_rope) + t * a.qr_t + h * a.qr_h + col * 8, ok);
+    }
+  }
   int32_t seq = a.shared_seq;
   if (token < 0) {
     if (tid < kAttnRows) {
       int32_t n = 0;
       if (tid < rows) {
-        const int32_t t = static_cast<int32_t>((row0 + tid) / a.H);
+        const int32_t t = (row0 + tid) / a.H;
         n = token_limit(a, t, token_seq(a, t));
       }
       sh.limit[tid] = n;
@@ -181,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
     }
   } else {
     seq = token_seq(a, token);
-    if (a.idx == nullptr) {
+    if (idx == nullptr) {
       const int32_t n = token_limit(a, token, seq);
       if (tid < kAttnRows) sh.limit[tid] = n;
       if (tid == 0) sh.key_end = min(n, k1);
@@ -189,162 +216,187 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       // entries behind the last valid one (short histories are padded) are not visited
       if (tid < kAttnRows) sh.limit[tid] = 0x7FFFFFFF;
       int32_t last = 0;
-      if (seq >= 0)
-        for (int32_t k = k0 + tid; k < k1; k += kThreads)
-          if (a.idx[static_cast<int64_t>(token) * a.top_k + k] >= 0) last = k + 1;
-      last = __reduce_max_sync(0xffffffffu, last);
-      if (lane == 0) atomicMax(&sh.key_end, last);
+      for (int32_t k = k0 + tid; k < k1; k += kThreads)
+        if (idx[k] >= 0) last = k + 1;
+      last = __reduce_max_sync(0xffffffffu, seq < 0 ? 0 : last);
+      if (lane == 0 && last > 0) atomicMax(&sh.key_end, last);
     }
   }
   __syncthreads();
   const int32_t key_end = sh.key_end;
   const int tiles = key_end > k0 ? (key_end - k0 + kAttnTile - 1) / kAttnTile : 0;
-  const int blocks = a.kv.rope ? kBlocks : kBlocks - 1;
   tc_fence_after();
-  const uint32_t tmem = sh.tmem;
 
-  if (warp >= kMmaWarp + 1) {
+  if (lw >= 0) {
     // ---------------------------------------------------------------- loads
-    const int lw = warp - kMmaWarp - 1;                  // rows 8 lw .. 8 lw + 7 of every block
-    const int sub = lane >> 3, col = lane & 7;           // a lane's 16-byte column, rows sub and sub + 4
-    if (tiles > 0) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = lw * 8 + sub + 4 * j;
-        const bool ok = r < rows;
-        const int64_t qr = row0 + (ok ? r : 0);
-        const int64_t t = qr / a.H, h = qr % a.H;
-        const __nv_bfloat16* ql = static_cast<const __nv_bfloat16*>(a.q_latent) + t * a.ql_t + h * a.ql_h + col * 8;
-        const uint32_t dst = smem + kOffQ + r * 128 + ((col ^ (r & 7)) << 4);
-#pragma unroll
-        for (int c = 0; c < kBlocks - 1; ++c) cp_async16(dst + c * kBlock, ql + c * 64, ok);
-        if (blocks == kBlocks) {
-          const __nv_bfloat16* qx = static_cast<const __nv_bfloat16*>(a.q_rope) + t * a.qr_t + h * a.qr_h + col * 8;
-          cp_async16(dst + (kBlocks - 1) * kBlock, qx, ok);
-        }
-      }
-    }
-    int landed = 0, issued = 0;                          // tiles handed to the products, tiles under way
-    auto hand_over = [&](int i) {
+    auto arrive = [&](int i, int h) {
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.full[i % kStages]);
+      if (lane == 0) mbar_arrive(&sh.full[i % kStages][h]);
     };
-    for (int i = 0; i < tiles; ++i) {
-      const int st = i % kStages;
-      // the cache rows of this warp's 8 keys, one per lane (all lanes hold one of them)
+    // the cache row of this warp's key `col` of tile i (-1: none), the same in the lanes of one column
+    auto lookup = [&](int i) -> int32_t {
       const int32_t k = k0 + i * kAttnTile + lw * 8 + col;
       int32_t pos = -1;
-      if (k < key_end) pos = a.idx ? a.idx[static_cast<int64_t>(token) * a.top_k + k] : k;
-      int64_t row = -1;
-      if (pos >= 0) row = cache_row(a.kv, seq, pos, a.err, token < 0 ? static_cast<int>(row0 / a.H) : token);
+      if (k < key_end) pos = idx ? idx[k] : k;
+      return pos < 0 ? -1 : cache_row(a.kv, seq, pos, a.err, token < 0 ? row0 / a.H : token);
+    };
+    int32_t row = tiles > 0 ? lookup(0) : -1;
+    bool ok = true;
+    for (int i = 0; i < tiles; ++i) {
+      const int st = i % kStages;
+      const uint32_t parity = ((i / kStages) - 1) & 1;
+      const uint32_t stage = smem + kOffK + st * kStage;
       const uint32_t valid = __ballot_sync(0xffffffffu, row >= 0) & 0xFFu;
-      uint4 codes[8];
+      uint4 codes[2][4];
       float scale = 0.f;
       if constexpr (FP8) {
+        // lane: row 2 j + lane / 16, 16 codes from 16 (lane % 16) of each half
         if (row >= 0) scale = a.kv.scale[row];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int64_t rj = __shfl_sync(0xffffffffu, row, j);
-          codes[j] = make_uint4(0u, 0u, 0u, 0u);
-          if (rj >= 0) codes[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.kv.latent) + rj * kLatentDim) + lane);
-        }
-      }
-      if (i >= kStages) {
-        for (; landed < i; ++landed) {                    // nothing may wait behind this wait
-          cp_async_wait<0>();
-          hand_over(landed);
-        }
-        const bool free_again = mbar_wait<true>(&sh.empty[st], ((i / kStages) - 1) & 1, &sh.abort);
-        if (!__all_sync(0xffffffffu, free_again)) break;  // a warp leaves as one
-      }
-      if (lane == 0) sh.valid[st][lw] = static_cast<uint8_t>(valid);
-      const uint32_t stage = smem + kOffK + st * kStage;
+        for (int j = 0; j < 4; ++j) {
+          const int32_t rj = __shfl_sync(0xffffffffu, row, 2 * j + (lane >> 4));
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.kv.latent) + static_cast<int64_t>(rj) * kLatentDim) + (lane & 15);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r8 = sub + 4 * j;
-        const int64_t rj = __shfl_sync(0xffffffffu, row, r8);
-        const bool ok = rj >= 0;
-        const int64_t at = ok ? rj : 0;
-        const uint32_t dst = stage + (lw * 8 + r8) * 128 + ((col ^ r8) << 4);
+          for (int h = 0; h < 2; ++h) codes[h][j] = rj >= 0 ? __ldg(src + 16 * h) : make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (i >= kStages) {
+          ok = mbar_wait<true>(&sh.empty[st][h], parity, &sh.abort);
+          ok = __all_sync(0xffffffffu, ok);              // a warp leaves as one
+          if (!ok) break;
+        }
+        if (h == 1 && lane == 0) sh.valid[st][lw] = static_cast<uint8_t>(valid);
         if constexpr (!FP8) {
-          const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.kv.latent) + at * kLatentDim + col * 8;
 #pragma unroll
-          for (int c = 0; c < kBlocks - 1; ++c) cp_async16(dst + c * kBlock, src + c * 64, ok);
-        }
-        if (blocks == kBlocks)
-          cp_async16(dst + (kBlocks - 1) * kBlock, static_cast<const __nv_bfloat16*>(a.kv.rope) + at * kLatentRope + col * 8, ok);
-      }
-      cp_async_commit();
-      if constexpr (FP8) {
-        // lane l holds values 16 l .. 16 l + 15 of a row: two 16-byte columns of block l / 4.  Lanes of odd blocks
-        // store the second one first, so that the eight lanes of a store's phase fall on different banks.
-        const int swap = (lane >> 2) & 1;
+          for (int j = 0; j < 2; ++j) {
+            const int r8 = sub + 4 * j;
+            const int32_t rj = __shfl_sync(0xffffffffu, row, r8);
+            const uint32_t dst = stage + h * kHalf * kBlock + (lw * 8 + r8) * 128 + ((col ^ r8) << 4);
+            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.kv.latent) + static_cast<int64_t>(max(rj, 0)) * kLatentDim + h * 256 + col * 8;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float s = __shfl_sync(0xffffffffu, scale, j);
-          const uint32_t w[4] = {codes[j].x, codes[j].y, codes[j].z, codes[j].w};
-          uint32_t v[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[2 * e] = e4m3x2_to_bf16x2(w[e] & 0xFFFFu, s);
-            v[2 * e + 1] = e4m3x2_to_bf16x2(w[e] >> 16, s);
-          }
-          const uint32_t base = stage + (lane >> 2) * kBlock + (lw * 8 + j) * 128;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const int half = x ^ swap;
-            const uint32_t dst = base + ((((lane & 3) * 2 + half) ^ j) << 4);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(half ? v[4] : v[0]), "r"(half ? v[5] : v[1]),
-                         "r"(half ? v[6] : v[2]), "r"(half ? v[7] : v[3])
-                         : "memory");
+            for (int c = 0; c < kHalf; ++c) cp_async16(dst + c * kBlock, src + c * 64, rj >= 0);
           }
         }
+        if (h == 1 && a.kv.rope) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int r8 = sub + 4 * j;
+            const int32_t rj = __shfl_sync(0xffffffffu, row, r8);
+            cp_async16(stage + kWeights + (lw * 8 + r8) * 128 + ((col ^ r8) << 4),
+                       static_cast<const __nv_bfloat16*>(a.kv.rope) + static_cast<int64_t>(max(rj, 0)) * kLatentRope + col * 8, rj >= 0);
+          }
+        }
+        cp_async_commit();
+        if constexpr (FP8) {
+          // two 16-byte columns of block (lane % 16) / 4.  Lanes of odd blocks store the second one first, so that
+          // the eight lanes of a store's phase fall on different banks.
+          const int swap = (lane >> 2) & 1;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r8 = 2 * j + (lane >> 4);
+            const float s = __shfl_sync(0xffffffffu, scale, r8);
+            const uint32_t w[4] = {codes[h][j].x, codes[h][j].y, codes[h][j].z, codes[h][j].w};
+            uint32_t v[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              v[2 * e] = e4m3x2_to_bf16x2(w[e] & 0xFFFFu, s);
+              v[2 * e + 1] = e4m3x2_to_bf16x2(w[e] >> 16, s);
+            }
+            const uint32_t base = stage + (h * kHalf + ((lane & 15) >> 2)) * kBlock + (lw * 8 + r8) * 128;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int second = x ^ swap;
+              const uint32_t dst = base + ((((lane & 3) * 2 + second) ^ r8) << 4);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(second ? v[4] : v[0]), "r"(second ? v[5] : v[1]),
+                           "r"(second ? v[6] : v[2]), "r"(second ? v[7] : v[3])
+                           : "memory");
+            }
+          }
+          if (h == 0 && i > 0) arrive(i, 0);             // only the first tile's queries are still under way
+        }
       }
-      ++issued;
-      if (i == 1) {                                       // the first tile need not wait for the second
-        cp_async_wait<1>();
-        hand_over(0);
-        landed = 1;
+      if (!ok) break;
+      const int32_t next = i + 1 < tiles ? lookup(i + 1) : -1;
+      if (next >= 0) {
+        // the next tile's rows towards the L2 while this one lands: 128-byte lines, spread over the lanes of a column
+        const char* line = static_cast<const char*>(a.kv.latent) + static_cast<int64_t>(next) * (FP8 ? kLatentDim : 2 * kLatentDim);
+#pragma unroll
+        for (int x = 0; x < (FP8 ? 1 : 2); ++x) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + (sub + 4 * x) * 128));
+        if (a.kv.rope && sub == 0)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.kv.rope) + static_cast<int64_t>(next) * (2 * kLatentRope)));
       }
+      if (!FP8 || i == 0) {
+        cp_async_wait<1>();                              // the queries were committed with the first half
+        arrive(i, 0);
+      }
+      cp_async_wait<0>();
+      arrive(i, 1);
+      row = next;
     }
     cp_async_wait<0>();
-    if (issued == tiles)
-      for (; landed < tiles; ++landed) hand_over(landed);
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- products
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idesc_s = make_idesc(1, kAttnRows, kAttnTile);
       constexpr uint32_t idesc_o = make_idesc(1, kAttnRows, 256) | kIdescBMnMajor;
-      bool ok = true;
-      auto second = [&](int i) {
-        if (!mbar_wait(&sh.weights, i & 1, &sh.abort)) return false;
-        tc_fence_after();
-        const uint32_t stage = smem + kOffK + (i % kStages) * kStage;
+      int q = 0, v = 0;                                  // next tiles of the first and of the second product
+      int half = 0;                                      // halves of tile q's first product already issued
+      long long since = clock64();
+      while (v < tiles) {
+        // a score tile is free once the second product of the tile before last has its weights
+        if (q < tiles && q - v < 2 && mbar_test(&sh.full[q % kStages][half], (q / kStages) & 1)) {
+          tc_fence_after();
+          const uint32_t stage = smem + kOffK + (q % kStages) * kStage;
+          const uint32_t d = kTmemS + (q & 1) * kAttnTile;
+          if (half == 0) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+            for (int c = 0; c < kHalf; ++c)
 #pragma unroll
-          for (int ks = 0; ks < kAttnTile / 16; ++ks)
-            umma_f16(tmem + kTmemO + half * kUpperLanes, sdesc_kmajor_sw128(smem + kOffP + ks * 32),
-                     sdesc_mnmajor_sw128(stage + half * 4 * kBlock + ks * 2048, kBlock), idesc_o, i > 0 || ks > 0);
-        umma_commit(&sh.empty[i % kStages]);
-        return true;
-      };
-      for (int i = 0; i < tiles && ok; ++i) {
-        ok = mbar_wait(&sh.full[i % kStages], (i / kStages) & 1, &sh.abort);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t stage = smem + kOffK + (i % kStages) * kStage;
-        const uint32_t d = tmem + kTmemS + (i & 1) * kAttnTile;
-        for (int c = 0; c < blocks; ++c)
+              for (int ks = 0; ks < 4; ++ks)
+                umma_f16(d, sdesc_kmajor_sw128(smem + c * kBlock + ks * 32),
+                         sdesc_kmajor_sw128(stage + c * kBlock + ks * 32), idesc_s, c > 0 || ks > 0);
+            half = 1;
+          } else {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_f16(d, sdesc_kmajor_sw128(smem + kOffQ + c * kBlock + ks * 32),
-                     sdesc_kmajor_sw128(stage + c * kBlock + ks * 32), idesc_s, c > 0 || ks > 0);
-        umma_commit(&sh.scores[i & 1]);
-        if (i > 0) ok = second(i - 1);
+            for (int c = kHalf; c < kLatentBlocks; ++c)
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                umma_f16(d, sdesc_kmajor_sw128(smem + c * kBlock + ks * 32),
+                         sdesc_kmajor_sw128(stage + c * kBlock + ks * 32), idesc_s, 1);
+            if (a.kv.rope) {
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                umma_f16(d, sdesc_kmajor_sw128(smem + kWeights + ks * 32),
+                         sdesc_kmajor_sw128(stage + kWeights + ks * 32), idesc_s, 1);
+            }
+            umma_commit(&sh.scores[q & 1]);
+            half = 0;
+            ++q;
+          }
+          since = clock64();
+        } else if (v < q && mbar_test(&sh.weights[v & 1], (v >> 1) & 1)) {
+          tc_fence_after();
+          const uint32_t stage = smem + kOffK + (v % kStages) * kStage;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int ks = 0; ks < kAttnTile / 16; ++ks)
+              umma_f16(kTmemO + h * kUpperLanes, sdesc_kmajor_sw128(stage + kWeights + ks * 32),
+                       sdesc_mnmajor_sw128(stage + h * kHalf * kBlock + ks * 2048, kBlock), idesc_o, v > 0 || ks > 0);
+            umma_commit(&sh.empty[v % kStages][h]);
+          }
+          ++v;
+          since = clock64();
+        } else if (*const_cast<volatile int*>(&sh.abort)) {
+          break;
+        } else if (clock64() - since > kWaitLimitCycles) {
+          *const_cast<volatile int*>(&sh.abort) = 1;
+          break;
+        }
       }
-      if (ok && tiles > 0) ok = second(tiles - 1);
       umma_commit(&sh.drained);
       int alone = 0;                                     // also after an abort: nothing may run on freed tensor memory
       mbar_wait(&sh.drained, 0, &alone);
@@ -355,12 +407,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
     // The thread's two rows of the score tile: lane / 4 and lane / 4 + 8 of the warp's 16, 16 columns of each.
     const int fr = lane >> 2;
     const int32_t limit[2] = {sh.limit[warp * 16 + fr], sh.limit[warp * 16 + fr + 8]};
-    const uint32_t quadrant = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t quadrant = static_cast<uint32_t>(warp * 32) << 16;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     bool ok = true;
     for (int i = 0; i < tiles; ++i) {
       ok = mbar_wait<true>(&sh.scores[i & 1], (i >> 1) & 1, &sh.abort);
-      ok = ok && mbar_wait<true>(&sh.full[i % kStages], (i / kStages) & 1, &sh.abort);   // for `valid`
+      ok = ok && mbar_wait<true>(&sh.full[i % kStages][1], (i / kStages) & 1, &sh.abort);   // for `valid`
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -414,50 +466,42 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
           m[r] = mn;
         }
       }
-      uint32_t w[2][8];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float ref = m[r] == -INFINITY ? 0.f : m[r];
+        const uint32_t dst = smem + kOffK + (i % kStages) * kStage + kWeights + (warp * 16 + fr + 8 * r) * 128 + (lane & 3) * 4;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float lo = exp2_fast(x[r][2 * j] - ref), hi = exp2_fast(x[r][2 * j + 1] - ref);
-          l[r] += lo + hi;
-          w[r][j] = bf16x2(lo, hi);                      // the sum keeps fp32; the product's operand is bf16
+          l[r] += lo + hi;                               // the sum keeps fp32; the product's operand is bf16
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + ((j ^ fr) << 4)), "r"(bf16x2(lo, hi)) : "memory");
         }
       }
-      if (i > 0) {                                       // the weights' buffer and the output are free again
-        ok = mbar_wait<true>(&sh.empty[(i - 1) % kStages], ((i - 1) / kStages) & 1, &sh.abort);
+      if (rescale && i > 0) {
+        // the output of the tiles before this one, complete, times the factor
+        ok = mbar_wait<true>(&sh.empty[(i - 1) % kStages][1], ((i - 1) / kStages) & 1, &sh.abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (rescale) {
-          tc_fence_after();
-          // an output lane's row is lane % 16: its factor sits with the lanes 4 (row % 8) of the score layout
-          const float f0 = __shfl_sync(0xffffffffu, factor[0], (lane & 7) * 4);
-          const float f1 = __shfl_sync(0xffffffffu, factor[1], (lane & 7) * 4);
-          const float f = lane & 8 ? f1 : f0;
+        tc_fence_after();
+        // an output lane's row is lane % 16: its factor sits with the lanes 4 (row % 8) of the score layout
+        const float f0 = __shfl_sync(0xffffffffu, factor[0], (lane & 7) * 4);
+        const float f1 = __shfl_sync(0xffffffffu, factor[1], (lane & 7) * 4);
+        const float f = lane & 8 ? f1 : f0;
 #pragma unroll 1
-          for (int c = 0; c < 256; c += 32) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(quadrant + kTmemO + c, o);
-            tmem_ld_wait();
+        for (int c = 0; c < 256; c += 32) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(quadrant + kTmemO + c, o);
+          tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st_32x32b_x32(quadrant + kTmemO + c, o);
-          }
-          tmem_st_wait();
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+          tmem_st_32x32b_x32(quadrant + kTmemO + c, o);
         }
-      }
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint32_t dst = smem + kOffP + (warp * 16 + fr + 8 * r) * 128 + (lane & 3) * 4;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + ((j ^ fr) << 4)), "r"(w[r][j]) : "memory");
+        tmem_st_wait();
       }
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.weights);
+      if (lane == 0) mbar_arrive(&sh.weights[i & 1]);
     }
     launch_dependents();
     // ---------------------------------------------------------------- the result
@@ -475,18 +519,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
     const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
     const int r = warp * 16 + (lane & 15);
     const bool mine = r < rows;
-    const int64_t R = static_cast<int64_t>(a.T) * a.H;
-    const int64_t orow = p.slots() == 1 ? row0 + r : slot * R + row0 + r;
+    const bool parts = p.slots() > 1;
+    const int64_t orow = (parts ? static_cast<int64_t>(slot) * a.T * a.H : 0) + row0 + r;
     if (tiles > 0 && ok) {
-      ok = mbar_wait<true>(&sh.empty[(tiles - 1) % kStages], ((tiles - 1) / kStages) & 1, &sh.abort);
+      // every product of the CTA: the stages take the result next
+      ok = mbar_wait<true>(&sh.empty[(tiles - 1) % kStages][1], ((tiles - 1) / kStages) & 1, &sh.abort);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
     }
     if (ok && mine && lane < 16) {
-      if (p.slots() > 1) a.part_lse[orow] = lse2;
+      if (parts) a.part_lse[orow] = lse2;
       else if (a.lse) a.lse[orow] = lse2 * kLn2;
     }
-    if (ok && (tiles > 0 || p.slots() == 1)) {
+    if (ok && (tiles > 0 || !parts)) {
+      const uint32_t stride = parts ? kOutRow32 : kOutRow16;
+      const uint32_t mem = smem + kOffK + r * stride + (lane >> 4) * (parts ? 1024 : 512);
 #pragma unroll 1
       for (int c = 0; c < 256; c += 32) {
         uint32_t o[32];
@@ -497,30 +544,42 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
-        if (!mine) continue;
-        const int64_t at = orow * kLatentDim + (lane >> 4) * 256 + c;
         // a row without keys is zero whatever its weights' products with foreign keys left
-        auto val = [&](int e) { return sum == 0.f ? 0.f : __uint_as_float(o[e]) * inv; };
-        if (p.slots() == 1) {
-          uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at);
+        float val[32];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            out[e] = make_uint4(bf16x2(val(8 * e), val(8 * e + 1)), bf16x2(val(8 * e + 2), val(8 * e + 3)),
-                                bf16x2(val(8 * e + 4), val(8 * e + 5)), bf16x2(val(8 * e + 6), val(8 * e + 7)));
+        for (int e = 0; e < 32; ++e) val[e] = sum == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
+        if (parts) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mem + (c + e) * 4), "f"(val[e]), "f"(val[e + 1]),
+                         "f"(val[e + 2]), "f"(val[e + 3])
+                         : "memory");
         } else {
-          float4* out = reinterpret_cast<float4*>(a.part_o + at);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) out[e] = make_float4(val(4 * e), val(4 * e + 1), val(4 * e + 2), val(4 * e + 3));
+          for (int e = 0; e < 32; e += 8)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mem + (c + e) * 2), "r"(bf16x2(val[e], val[e + 1])),
+                         "r"(bf16x2(val[e + 2], val[e + 3])), "r"(bf16x2(val[e + 4], val[e + 5])),
+                         "r"(bf16x2(val[e + 6], val[e + 7]))
+                         : "memory");
         }
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (mine && lane < 16) {                           // a row each, whole
+        if (parts)
+          bulk_store(a.part_o + orow * kLatentDim, smem + kOffK + r * kOutRow32, kLatentDim * 4);
+        else
+          bulk_store(static_cast<__nv_bfloat16*>(a.out) + orow * kLatentDim, smem + kOffK + r * kOutRow16, kLatentDim * 2);
+      }
+      bulk_store_wait_read();
     }
   }
-  if (sh.abort && lane == 0) record_error(a.err, DSA_DEVERR_TIMEOUT, static_cast<int>(blockIdx.x));
+  if (*const_cast<volatile int*>(&sh.abort) && lane == 0) record_error(a.err, DSA_DEVERR_TIMEOUT, static_cast<int>(blockIdx.x));
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(sh.tmem, kTmemCols);
   }
 }
 
