@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -216,8 +217,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       // entries behind the last valid one (short histories are padded) are not visited
       if (tid < kAttnRows) sh.limit[tid] = 0x7FFFFFFF;
       int32_t last = 0;
-      for (int32_t k = k0 + tid; k < k1; k += kThreads)
-        if (idx[k] >= 0) last = k + 1;
+      for (int32_t k = k0 + tid; k < k1; k += 8 * kThreads) {
+        int32_t e[8];                                    // loads side by side
+#pragma unroll
+        for (int x = 0; x < 8; ++x) e[x] = k + x * kThreads < k1 ? idx[k + x * kThreads] : -1;
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (e[x] >= 0) last = k + x * kThreads + 1;
+      }
       last = __reduce_max_sync(0xffffffffu, seq < 0 ? 0 : last);
       if (lane == 0 && last > 0) atomicMax(&sh.key_end, last);
     }
@@ -241,25 +248,54 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       if (k < key_end) pos = idx ? idx[k] : k;
       return pos < 0 ? -1 : cache_row(a.kv, seq, pos, a.err, token < 0 ? row0 / a.H : token);
     };
+    // 16 FP8 codes of each half of four of the warp's rows: row 2 j + lane / 16, codes from 16 (lane % 16)
+    uint4 codes[2][4];
+    float scale = 0.f;
+    auto fetch = [&](int32_t row) {
+      scale = row >= 0 ? a.kv.scale[row] : 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int32_t rj = __shfl_sync(0xffffffffu, row, 2 * j + (lane >> 4));
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.kv.latent) + static_cast<int64_t>(rj) * kLatentDim) + (lane & 15);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) codes[h][j] = rj >= 0 ? __ldg(src + 16 * h) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
     int32_t row = tiles > 0 ? lookup(0) : -1;
+    if constexpr (FP8) fetch(row);
     bool ok = true;
     for (int i = 0; i < tiles; ++i) {
       const int st = i % kStages;
       const uint32_t parity = ((i / kStages) - 1) & 1;
       const uint32_t stage = smem + kOffK + st * kStage;
       const uint32_t valid = __ballot_sync(0xffffffffu, row >= 0) & 0xFFu;
-      uint4 codes[2][4];
-      float scale = 0.f;
+      uint32_t wide[2][4][8];                            // the codes' values in bf16
       if constexpr (FP8) {
-        // lane: row 2 j + lane / 16, 16 codes from 16 (lane % 16) of each half
-        if (row >= 0) scale = a.kv.scale[row];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int32_t rj = __shfl_sync(0xffffffffu, row, 2 * j + (lane >> 4));
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.kv.latent) + static_cast<int64_t>(rj) * kLatentDim) + (lane & 15);
+          const float s = __shfl_sync(0xffffffffu, scale, 2 * j + (lane >> 4));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) codes[h][j] = rj >= 0 ? __ldg(src + 16 * h) : make_uint4(0u, 0u, 0u, 0u);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t w[4] = {codes[h][j].x, codes[h][j].y, codes[h][j].z, codes[h][j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              wide[h][j][2 * e] = e4m3x2_to_bf16x2(w[e] & 0xFFFFu, s);
+              wide[h][j][2 * e + 1] = e4m3x2_to_bf16x2(w[e] >> 16, s);
+            }
+          }
         }
+      }
+      // the next tile's rows, before the wait for this tile's place: FP8 into registers, bf16 towards the L2
+      // (128-byte lines, spread over the lanes of a column)
+      const int32_t next = i + 1 < tiles ? lookup(i + 1) : -1;
+      if constexpr (FP8) {
+        if (i + 1 < tiles) fetch(next);
+      } else if (next >= 0) {
+        const char* line = static_cast<const char*>(a.kv.latent) + static_cast<int64_t>(next) * (2 * kLatentDim) + sub * 128;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(line + 512));
+        if (a.kv.rope && sub == 0)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.kv.rope) + static_cast<int64_t>(next) * (2 * kLatentRope)));
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -297,14 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int r8 = 2 * j + (lane >> 4);
-            const float s = __shfl_sync(0xffffffffu, scale, r8);
-            const uint32_t w[4] = {codes[h][j].x, codes[h][j].y, codes[h][j].z, codes[h][j].w};
-            uint32_t v[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              v[2 * e] = e4m3x2_to_bf16x2(w[e] & 0xFFFFu, s);
-              v[2 * e + 1] = e4m3x2_to_bf16x2(w[e] >> 16, s);
-            }
+            const uint32_t* v = wide[h][j];
             const uint32_t base = stage + (h * kHalf + ((lane & 15) >> 2)) * kBlock + (lw * 8 + r8) * 128;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -319,15 +348,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
         }
       }
       if (!ok) break;
-      const int32_t next = i + 1 < tiles ? lookup(i + 1) : -1;
-      if (next >= 0) {
-        // the next tile's rows towards the L2 while this one lands: 128-byte lines, spread over the lanes of a column
-        const char* line = static_cast<const char*>(a.kv.latent) + static_cast<int64_t>(next) * (FP8 ? kLatentDim : 2 * kLatentDim);
-#pragma unroll
-        for (int x = 0; x < (FP8 ? 1 : 2); ++x) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + (sub + 4 * x) * 128));
-        if (a.kv.rope && sub == 0)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.kv.rope) + static_cast<int64_t>(next) * (2 * kLatentRope)));
-      }
       if (!FP8 || i == 0) {
         cp_async_wait<1>();                              // the queries were committed with the first half
         arrive(i, 0);
@@ -344,50 +364,57 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       constexpr uint32_t idesc_o = make_idesc(1, kAttnRows, 256) | kIdescBMnMajor;
       int q = 0, v = 0;                                  // next tiles of the first and of the second product
       int half = 0;                                      // halves of tile q's first product already issued
+      // S[st] (+)= Q K[st]^T over one half of the values (the second with the rotated part), the stage a constant
+      auto first = [&](auto st, auto h) {
+        constexpr uint32_t stage = kOffK + decltype(st)::value * kStage;
+        constexpr uint32_t d = kTmemS + decltype(st)::value * kAttnTile;
+        constexpr int c0 = decltype(h)::value * kHalf;
+#pragma unroll
+        for (int c = c0; c < c0 + kHalf; ++c)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_f16(d, sdesc_kmajor_sw128(smem + c * kBlock + ks * 32),
+                     sdesc_kmajor_sw128(smem + stage + c * kBlock + ks * 32), idesc_s, c > 0 || ks > 0);
+        if constexpr (c0 > 0) {
+          if (a.kv.rope) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_f16(d, sdesc_kmajor_sw128(smem + kWeights + ks * 32),
+                       sdesc_kmajor_sw128(smem + stage + kWeights + ks * 32), idesc_s, 1);
+          }
+          umma_commit(&sh.scores[decltype(st)::value]);
+        }
+      };
+      auto second = [&](auto st, uint32_t accumulate) {
+        constexpr uint32_t stage = kOffK + decltype(st)::value * kStage;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int ks = 0; ks < kAttnTile / 16; ++ks)
+            umma_f16(kTmemO + h * kUpperLanes, sdesc_kmajor_sw128(smem + stage + kWeights + ks * 32),
+                     sdesc_mnmajor_sw128(smem + stage + h * kHalf * kBlock + ks * 2048, kBlock), idesc_o, ks > 0 ? 1u : accumulate);
+          umma_commit(&sh.empty[decltype(st)::value][h]);
+        }
+      };
+      constexpr std::integral_constant<int, 0> c0{};
+      constexpr std::integral_constant<int, 1> c1{};
       long long since = clock64();
       while (v < tiles) {
         // a score tile is free once the second product of the tile before last has its weights
         if (q < tiles && q - v < 2 && mbar_test(&sh.full[q % kStages][half], (q / kStages) & 1)) {
           tc_fence_after();
-          const uint32_t stage = smem + kOffK + (q % kStages) * kStage;
-          const uint32_t d = kTmemS + (q & 1) * kAttnTile;
           if (half == 0) {
-#pragma unroll
-            for (int c = 0; c < kHalf; ++c)
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                umma_f16(d, sdesc_kmajor_sw128(smem + c * kBlock + ks * 32),
-                         sdesc_kmajor_sw128(stage + c * kBlock + ks * 32), idesc_s, c > 0 || ks > 0);
+            if (q & 1) first(c1, c0); else first(c0, c0);
             half = 1;
           } else {
-#pragma unroll
-            for (int c = kHalf; c < kLatentBlocks; ++c)
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                umma_f16(d, sdesc_kmajor_sw128(smem + c * kBlock + ks * 32),
-                         sdesc_kmajor_sw128(stage + c * kBlock + ks * 32), idesc_s, 1);
-            if (a.kv.rope) {
-#pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                umma_f16(d, sdesc_kmajor_sw128(smem + kWeights + ks * 32),
-                         sdesc_kmajor_sw128(stage + kWeights + ks * 32), idesc_s, 1);
-            }
-            umma_commit(&sh.scores[q & 1]);
+            if (q & 1) first(c1, c1); else first(c0, c1);
             half = 0;
             ++q;
           }
           since = clock64();
         } else if (v < q && mbar_test(&sh.weights[v & 1], (v >> 1) & 1)) {
           tc_fence_after();
-          const uint32_t stage = smem + kOffK + (v % kStages) * kStage;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int ks = 0; ks < kAttnTile / 16; ++ks)
-              umma_f16(kTmemO + h * kUpperLanes, sdesc_kmajor_sw128(stage + kWeights + ks * 32),
-                       sdesc_mnmajor_sw128(stage + h * kHalf * kBlock + ks * 2048, kBlock), idesc_o, v > 0 || ks > 0);
-            umma_commit(&sh.empty[v % kStages][h]);
-          }
+          if (v & 1) second(c1, 1u); else second(c0, v > 0);
           ++v;
           since = clock64();
         } else if (*const_cast<volatile int*>(&sh.abort)) {
@@ -434,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) x[r][2 * j + e] = __uint_as_float(raw[4 * j + 2 * r + e]) * a.scale_log2;
+          for (int e = 0; e < 2; ++e) x[r][2 * j + e] = __uint_as_float(raw[4 * j + 2 * r + e]);
       if (!whole) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -453,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
 #pragma unroll
         for (int e = 1; e < 16; ++e) mx[r] = fmaxf(mx[r], x[r][e]);
         mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2)) * a.scale_log2;   // the scale is positive
       }
       const bool rescale = __any_sync(0xffffffffu, mx[0] > m[0] + kLag || mx[1] > m[1] + kLag);
       float factor[2] = {1.f, 1.f};
@@ -472,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
         const uint32_t dst = smem + kOffK + (i % kStages) * kStage + kWeights + (warp * 16 + fr + 8 * r) * 128 + (lane & 3) * 4;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float lo = exp2_fast(x[r][2 * j] - ref), hi = exp2_fast(x[r][2 * j + 1] - ref);
+          const float lo = exp2_fast(fmaf(x[r][2 * j], a.scale_log2, -ref)), hi = exp2_fast(fmaf(x[r][2 * j + 1], a.scale_log2, -ref));
           l[r] += lo + hi;                               // the sum keeps fp32; the product's operand is bf16
           asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + ((j ^ fr) << 4)), "r"(bf16x2(lo, hi)) : "memory");
         }

@@ -137,6 +137,7 @@ def test_append_refusals(lib, change, expect):
     (dict(sh=516), "INVALID_ARG"), (dict(T=1 << 24, H=128), "UNSUPPORTED"), (dict(seq=None), "INVALID_ARG"),
     (dict(idx=None), "INVALID_ARG"), (dict(out=None), "INVALID_ARG"), (dict(out=0x800008), "INVALID_ARG"),
     (dict(scale=float("nan")), "INVALID_ARG"), (dict(scale=float("inf")), "INVALID_ARG"),
+    (dict(scale=0.0), "INVALID_ARG"), (dict(scale=-0.1), "INVALID_ARG"),
 ])
 def test_attention_refusals(lib, change, expect):
     a = dict(T=4, H=128, latent=0x400000, qrope=0x500000, st=65536, sh=512, seq=0x600000, idx=0x700000, out=0x800000, scale=0.1)
