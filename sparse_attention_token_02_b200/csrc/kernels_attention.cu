@@ -20,16 +20,19 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Cache row of position p of sequence seq, or -1 (reported) where the page table has no page for it.
-__device__ __forceinline__ int32_t cache_row(const LatentView& kv, int32_t seq, int32_t p, int* err, int info) {
+// The page table's entry for position p (>= 0) of sequence seq: -1 past its columns.
+__device__ __forceinline__ int32_t page_entry(const LatentView& kv, int32_t seq, int32_t p) {
   const int32_t slot = p / kv.page_size;
-  int32_t page = -1;
-  if (slot < kv.max_pages) page = kv.pages[static_cast<int64_t>(seq) * kv.max_pages + slot];
+  return slot < kv.max_pages ? __ldg(kv.pages + static_cast<int64_t>(seq) * kv.max_pages + slot) : -1;
+}
+
+// Cache row of position p on that page, or -1 (reported) where there is no such page.
+__device__ __forceinline__ int32_t page_row(const LatentView& kv, int32_t page, int32_t p, int* err, int info) {
   if (page < 0 || page >= kv.num_pages) {
     record_error(err, DSA_DEVERR_PAGE, info);
     return -1;
   }
-  return page * kv.page_size + (p - slot * kv.page_size);      // fewer than 2^31 rows
+  return page * kv.page_size + p % kv.page_size;         // fewer than 2^31 rows
 }
 
 // Sequence of token t: -1 for a padding token and (reported) for one outside the page table.
@@ -56,26 +59,30 @@ __device__ __forceinline__ int32_t token_limit(const AttnArgs& a, int32_t t, int
 // ------------------------------------------------------------------------------------------------ the pass
 
 // Shared memory of a CTA: operand blocks of 64 rows x 64 values (128-byte rows, 128-byte swizzle): the
-// queries, then two stages of keys.  A tile's weights take the place of its keys' rotated part, which
-// only the first product reads.
+// rotated part of the queries, then three stages of keys.
 constexpr uint32_t kBlock = 64 * 128;
 constexpr int kLatentBlocks = kLatentDim / 64;               // 8; the rotated part is a ninth
 constexpr int kHalf = kLatentBlocks / 2;                     // blocks per half: values 0 .. 255, 256 .. 511
 constexpr uint32_t kStage = (kLatentBlocks + 1) * kBlock;
-constexpr uint32_t kWeights = kLatentBlocks * kBlock;        // within a stage
-constexpr int kStages = 2;
-constexpr uint32_t kOffK = kStage;
+constexpr uint32_t kRotated = kLatentBlocks * kBlock;        // within a stage
+constexpr int kStages = 3;
+constexpr uint32_t kOffK = kBlock;
 constexpr uint32_t kSmemBytes = kOffK + kStages * kStage + 1024;   // 1024: the blocks' alignment
 // the result on its way out, over the keys' stages: rows of 512 fp32 or bf16 values, padded to spread the banks
 constexpr uint32_t kOutRow32 = kLatentDim * 4 + 16, kOutRow16 = kLatentDim * 2 + 16;
 static_assert(64 * kOutRow32 <= kStages * kStage, "the result must fit");
 
-// Tensor memory columns: the output's 512 columns as two accumulators of 256 (a 64-row accumulator fills
-// 16 of every 32 lanes: the values 0 .. 255 in the lower, 256 .. 511 in the upper 16), two score tiles.
+// Tensor memory.  A 64-row accumulator fills 16 of every 32 lanes, and a product's A operand in tensor memory
+// sits in the lanes of its result, so the values 0 .. 255 live in the lower 16 lanes and 256 .. 511 in
+// the upper 16: the queries (128 columns of bf16 pairs), the scores of either half of the values (64
+// columns, summed when they are read), the weights over the scores that they came from (once for each half),
+// and the output (256 columns).  Keeping queries and weights here leaves the shared memory's bandwidth, which
+// bounds a 64-row product with both operands in it, to the keys, and its room to a third stage.
 // All 512 columns are taken, so the allocation starts at column 0, a constant for the issuing thread.
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 0;
 constexpr uint32_t kTmemS = 256;
+constexpr uint32_t kTmemQ = 384;
 constexpr uint32_t kUpperLanes = 16u << 16;
 
 constexpr int kSoftmaxWarps = 4;
@@ -110,7 +117,8 @@ struct __align__(8) Shared {
   uint64_t full[kStages][2];    // a half of a tile's keys is in shared memory (the second half with the rotated part)
   uint64_t empty[kStages][2];   // a half of the tile's second product is done
   uint64_t scores[2];           // a score tile is complete
-  uint64_t weights[2];          // the weights of a tile are in shared memory, the output is rescaled
+  uint64_t weights[2];          // the weights of a tile are in tensor memory, the output is rescaled
+  uint64_t queries;             // the queries are in tensor memory
   uint64_t drained;             // every product of the CTA is done
   uint32_t tmem;
   int abort;
@@ -139,9 +147,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
           mbar_init(&sh.full[i][h], kLoadWarps);
           mbar_init(&sh.empty[i][h], 1);
         }
+      }
+      for (int i = 0; i < 2; ++i) {
         mbar_init(&sh.scores[i], 1);
         mbar_init(&sh.weights[i], kSoftmaxWarps);
       }
+      mbar_init(&sh.queries, kSoftmaxWarps);
       mbar_init(&sh.drained, 1);
       sh.abort = 0;
       sh.key_end = 0;
@@ -181,19 +192,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
   const int32_t* idx = a.idx ? a.idx + static_cast<int64_t>(token) * a.top_k : nullptr;
   const int lw = warp - kMmaWarp - 1;                    // loads: rows 8 lw .. 8 lw + 7 of every block
   const int sub = lane >> 3, col = lane & 7;             // a lane's 16-byte column, rows sub and sub + 4
-  if (lw >= 0) {
+  if (lw >= 0 && a.kv.rope) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {                        // the queries; they arrive with the first tile's second half
+    for (int j = 0; j < 2; ++j) {                        // the queries' rotated part, wanted with the first tile's
       const int r = lw * 8 + sub + 4 * j;
-      const bool ok = r < rows;
-      const int qr = row0 + (ok ? r : 0);
+      const int qr = row0 + (r < rows ? r : 0);
       const int t = qr / a.H, h = qr - t * a.H;
-      const __nv_bfloat16* ql = static_cast<const __nv_bfloat16*>(a.q_latent) + t * a.ql_t + h * a.ql_h + col * 8;
-      const uint32_t dst = smem + r * 128 + ((col ^ (r & 7)) << 4);
-#pragma unroll
-      for (int c = 0; c < kLatentBlocks; ++c) cp_async16(dst + c * kBlock, ql + c * 64, ok);
-      if (a.kv.rope)
-        cp_async16(dst + kWeights, static_cast<const __nv_bfloat16*>(a.q_rope) + t * a.qr_t + h * a.qr_h + col * 8, ok);
+      cp_async16(smem + r * 128 + ((col ^ (r & 7)) << 4),
+                 static_cast<const __nv_bfloat16*>(a.q_rope) + t * a.qr_t + h * a.qr_h + col * 8, r < rows);
     }
   }
   int32_t seq = a.shared_seq;
@@ -241,12 +247,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.full[i % kStages][h]);
     };
-    // the cache row of this warp's key `col` of tile i (-1: none), the same in the lanes of one column
-    auto lookup = [&](int i) -> int32_t {
+    // This warp's key `col` of a tile, the same in the lanes of one column: its position (-1: none) is read three
+    // tiles ahead, its page two, so that neither load is waited for.
+    auto position = [&](int i) -> int32_t {
       const int32_t k = k0 + i * kAttnTile + lw * 8 + col;
-      int32_t pos = -1;
-      if (k < key_end) pos = idx ? idx[k] : k;
-      return pos < 0 ? -1 : cache_row(a.kv, seq, pos, a.err, token < 0 ? row0 / a.H : token);
+      return k < key_end ? (idx ? __ldg(idx + k) : k) : -1;
+    };
+    auto page_of = [&](int32_t pos) -> int32_t { return pos < 0 ? -1 : page_entry(a.kv, seq, pos); };
+    auto row_of = [&](int32_t pos, int32_t page) -> int32_t {
+      return pos < 0 ? -1 : page_row(a.kv, page, pos, a.err, token < 0 ? row0 / a.H : token);
     };
     // 16 FP8 codes of each half of four of the warp's rows: row 2 j + lane / 16, codes from 16 (lane % 16)
     uint4 codes[2][4];
@@ -261,7 +270,25 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
         for (int h = 0; h < 2; ++h) codes[h][j] = rj >= 0 ? __ldg(src + 16 * h) : make_uint4(0u, 0u, 0u, 0u);
       }
     };
-    int32_t row = tiles > 0 ? lookup(0) : -1;
+    // Tiles under way are handed to the products when the warp would wait otherwise, oldest first.  Each has two
+    // groups of copies, one per half; an FP8 tile's first half has none and was handed over when it was written.
+    int landed = 0, issued = 0;
+    auto hand_over = [&] {
+      for (; landed < issued; ++landed) {
+        const int behind = issued - landed - 1;          // tiles issued after this one: fewer than the stages
+        if constexpr (!FP8) {
+          if (behind == 0) cp_async_wait<1>(); else if (behind == 1) cp_async_wait<3>(); else cp_async_wait<5>();
+          arrive(landed, 0);
+        }
+        if (behind == 0) cp_async_wait<0>(); else if (behind == 1) cp_async_wait<2>(); else cp_async_wait<4>();
+        arrive(landed, 1);
+      }
+    };
+    const int32_t pos0 = position(0), pos1 = position(1);
+    int32_t pos2 = position(2), pos3 = position(3);
+    const int32_t page0 = page_of(pos0), page1 = page_of(pos1);
+    int32_t page2 = page_of(pos2);
+    int32_t row = row_of(pos0, page0), next = row_of(pos1, page1);
     if constexpr (FP8) fetch(row);
     bool ok = true;
     for (int i = 0; i < tiles; ++i) {
@@ -285,18 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
           }
         }
       }
-      // the next tile's rows, before the wait for this tile's place: FP8 into registers, bf16 towards the L2
-      // (128-byte lines, spread over the lanes of a column)
-      const int32_t next = i + 1 < tiles ? lookup(i + 1) : -1;
-      if constexpr (FP8) {
-        if (i + 1 < tiles) fetch(next);
-      } else if (next >= 0) {
-        const char* line = static_cast<const char*>(a.kv.latent) + static_cast<int64_t>(next) * (2 * kLatentDim) + sub * 128;
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(line + 512));
-        if (a.kv.rope && sub == 0)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.kv.rope) + static_cast<int64_t>(next) * (2 * kLatentRope)));
-      }
+      if constexpr (FP8) fetch(next);                    // before the wait for this tile's place
+      if (i >= kStages && !__all_sync(0xffffffffu, mbar_test(&sh.empty[st][0], parity))) hand_over();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (i >= kStages) {
@@ -321,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
           for (int j = 0; j < 2; ++j) {
             const int r8 = sub + 4 * j;
             const int32_t rj = __shfl_sync(0xffffffffu, row, r8);
-            cp_async16(stage + kWeights + (lw * 8 + r8) * 128 + ((col ^ r8) << 4),
+            cp_async16(stage + kRotated + (lw * 8 + r8) * 128 + ((col ^ r8) << 4),
                        static_cast<const __nv_bfloat16*>(a.kv.rope) + static_cast<int64_t>(max(rj, 0)) * kLatentRope + col * 8, rj >= 0);
           }
         }
@@ -344,18 +361,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
                            : "memory");
             }
           }
-          if (h == 0 && i > 0) arrive(i, 0);             // only the first tile's queries are still under way
+          if (h == 0) arrive(i, 0);
         }
       }
       if (!ok) break;
-      if (!FP8 || i == 0) {
-        cp_async_wait<1>();                              // the queries were committed with the first half
-        arrive(i, 0);
-      }
-      cp_async_wait<0>();
-      arrive(i, 1);
+      ++issued;
       row = next;
+      next = row_of(pos2, page2);
+      page2 = page_of(pos3);
+      pos2 = pos3;
+      pos3 = position(i + 4);
     }
+    if (ok) hand_over();
     cp_async_wait<0>();
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- products
@@ -364,57 +381,71 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       constexpr uint32_t idesc_o = make_idesc(1, kAttnRows, 256) | kIdescBMnMajor;
       int q = 0, v = 0;                                  // next tiles of the first and of the second product
       int half = 0;                                      // halves of tile q's first product already issued
-      // S[st] (+)= Q K[st]^T over one half of the values (the second with the rotated part), the stage a constant
-      auto first = [&](auto st, auto h) {
+      // scores (+)= Q K[st]^T over one half of the values (the second with the rotated part), the stage a constant
+      auto first = [&](auto st, auto h, uint32_t d) {
         constexpr uint32_t stage = kOffK + decltype(st)::value * kStage;
-        constexpr uint32_t d = kTmemS + decltype(st)::value * kAttnTile;
-        constexpr int c0 = decltype(h)::value * kHalf;
+        constexpr int upper = decltype(h)::value;
 #pragma unroll
-        for (int c = c0; c < c0 + kHalf; ++c)
+        for (int c = 0; c < kHalf; ++c)
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            umma_f16(d, sdesc_kmajor_sw128(smem + c * kBlock + ks * 32),
-                     sdesc_kmajor_sw128(smem + stage + c * kBlock + ks * 32), idesc_s, c > 0 || ks > 0);
-        if constexpr (c0 > 0) {
+            umma_f16_ts(d + upper * kUpperLanes, kTmemQ + (c * 4 + ks) * 8 + upper * kUpperLanes,
+                        sdesc_kmajor_sw128(smem + stage + (upper * kHalf + c) * kBlock + ks * 32), idesc_s, c > 0 || ks > 0);
+        if constexpr (upper) {
           if (a.kv.rope) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              umma_f16(d, sdesc_kmajor_sw128(smem + kWeights + ks * 32),
-                       sdesc_kmajor_sw128(smem + stage + kWeights + ks * 32), idesc_s, 1);
+              umma_f16(d + kUpperLanes, sdesc_kmajor_sw128(smem + ks * 32),
+                       sdesc_kmajor_sw128(smem + stage + kRotated + ks * 32), idesc_s, 1);
           }
-          umma_commit(&sh.scores[decltype(st)::value]);
         }
       };
-      auto second = [&](auto st, uint32_t accumulate) {
+      auto second = [&](auto st, uint32_t w, uint32_t accumulate) {
         constexpr uint32_t stage = kOffK + decltype(st)::value * kStage;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
           for (int ks = 0; ks < kAttnTile / 16; ++ks)
-            umma_f16(kTmemO + h * kUpperLanes, sdesc_kmajor_sw128(smem + stage + kWeights + ks * 32),
-                     sdesc_mnmajor_sw128(smem + stage + h * kHalf * kBlock + ks * 2048, kBlock), idesc_o, ks > 0 ? 1u : accumulate);
+            umma_f16_ts(kTmemO + h * kUpperLanes, w + ks * 8 + h * kUpperLanes,
+                        sdesc_mnmajor_sw128(smem + stage + h * kHalf * kBlock + ks * 2048, kBlock), idesc_o, ks > 0 ? 1u : accumulate);
           umma_commit(&sh.empty[decltype(st)::value][h]);
         }
       };
       constexpr std::integral_constant<int, 0> c0{};
       constexpr std::integral_constant<int, 1> c1{};
+      constexpr std::integral_constant<int, 2> c2{};
+      int qs = 0, vs = 0;                                // their stages
+      uint32_t q_phase = 0;
+      if (tiles > 0) {
+        int* abort = &sh.abort;
+        mbar_wait(&sh.queries, 0, abort);
+        tc_fence_after();
+      }
       long long since = clock64();
       while (v < tiles) {
-        // a score tile is free once the second product of the tile before last has its weights
-        if (q < tiles && q - v < 2 && mbar_test(&sh.full[q % kStages][half], (q / kStages) & 1)) {
+        // a score tile is free once the second product of the tile before last, which reads its weights there, is issued
+        if (q < tiles && q - v < 2 && mbar_test(&sh.full[qs][half], q_phase)) {
           tc_fence_after();
+          const uint32_t d = kTmemS + (q & 1) * kAttnTile;
           if (half == 0) {
-            if (q & 1) first(c1, c0); else first(c0, c0);
+            if (qs == 0) first(c0, c0, d); else if (qs == 1) first(c1, c0, d); else first(c2, c0, d);
             half = 1;
           } else {
-            if (q & 1) first(c1, c1); else first(c0, c1);
+            if (qs == 0) first(c0, c1, d); else if (qs == 1) first(c1, c1, d); else first(c2, c1, d);
+            umma_commit(&sh.scores[q & 1]);
             half = 0;
             ++q;
+            if (++qs == kStages) {
+              qs = 0;
+              q_phase ^= 1;
+            }
           }
           since = clock64();
         } else if (v < q && mbar_test(&sh.weights[v & 1], (v >> 1) & 1)) {
           tc_fence_after();
-          if (v & 1) second(c1, 1u); else second(c0, v > 0);
+          const uint32_t w = kTmemS + (v & 1) * kAttnTile;
+          if (vs == 0) second(c0, w, v > 0); else if (vs == 1) second(c1, w, 1u); else second(c2, w, 1u);
+          if (++vs == kStages) vs = 0;
           ++v;
           since = clock64();
         } else if (*const_cast<volatile int*>(&sh.abort)) {
@@ -437,14 +468,42 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
     const uint32_t quadrant = static_cast<uint32_t>(warp * 32) << 16;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     bool ok = true;
+    if (tiles > 0) {
+      // the queries: a lane brings 256 values of the row lane % 16
+      const int r = warp * 16 + (lane & 15);
+      const int qr = row0 + (r < rows ? r : 0);
+      const int t = qr / a.H, h = qr - t * a.H;
+      const uint4* ql = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_latent) + t * a.ql_t + h * a.ql_h + (lane >> 4) * 256);
+#pragma unroll
+      for (int c = 0; c < 128; c += 64) {
+        uint4 x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = r < rows ? __ldg(ql + c / 4 + e) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          uint32_t v[32];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[4 * e] = x[8 * y + e].x; v[4 * e + 1] = x[8 * y + e].y; v[4 * e + 2] = x[8 * y + e].z; v[4 * e + 3] = x[8 * y + e].w;
+          }
+          tmem_st_32x32b_x32(quadrant + kTmemQ + c + 32 * y, v);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.queries);
+    }
     for (int i = 0; i < tiles; ++i) {
       ok = mbar_wait<true>(&sh.scores[i & 1], (i >> 1) & 1, &sh.abort);
       ok = ok && mbar_wait<true>(&sh.full[i % kStages][1], (i / kStages) & 1, &sh.abort);   // for `valid`
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      uint32_t raw[32];
-      tmem_ld_16x256b_x8(quadrant + kTmemS + (i & 1) * kAttnTile, raw);
+      const uint32_t tile = quadrant + kTmemS + (i & 1) * kAttnTile;
+      uint32_t raw[32], raw2[32];                        // the scores over either half of the values
+      tmem_ld_16x256b_x8(tile, raw);
+      tmem_ld_16x256b_x8(tile + kUpperLanes, raw2);
       const uint64_t present = *reinterpret_cast<const uint64_t*>(sh.valid[i % kStages]);
       tmem_ld_wait();
       float x[2][16];
@@ -461,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) x[r][2 * j + e] = __uint_as_float(raw[4 * j + 2 * r + e]);
+          for (int e = 0; e < 2; ++e) x[r][2 * j + e] = __uint_as_float(raw[4 * j + 2 * r + e]) + __uint_as_float(raw2[4 * j + 2 * r + e]);
       if (!whole) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -493,17 +552,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
           m[r] = mn;
         }
       }
+      uint32_t w[16];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float ref = m[r] == -INFINITY ? 0.f : m[r];
-        const uint32_t dst = smem + kOffK + (i % kStages) * kStage + kWeights + (warp * 16 + fr + 8 * r) * 128 + (lane & 3) * 4;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float lo = exp2_fast(fmaf(x[r][2 * j], a.scale_log2, -ref)), hi = exp2_fast(fmaf(x[r][2 * j + 1], a.scale_log2, -ref));
           l[r] += lo + hi;                               // the sum keeps fp32; the product's operand is bf16
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + ((j ^ fr) << 4)), "r"(bf16x2(lo, hi)) : "memory");
+          w[2 * j + r] = bf16x2(lo, hi);
         }
       }
+      tmem_st_16x128b_x8(tile, w);
+      tmem_st_16x128b_x8(tile + kUpperLanes, w);
       if (rescale && i > 0) {
         // the output of the tiles before this one, complete, times the factor
         ok = mbar_wait<true>(&sh.empty[(i - 1) % kStages][1], ((i - 1) / kStages) & 1, &sh.abort);
@@ -523,9 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
           tmem_st_32x32b_x32(quadrant + kTmemO + c, o);
         }
-        tmem_st_wait();
       }
-      fence_proxy_async_smem();
+      tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.weights[i & 1]);
