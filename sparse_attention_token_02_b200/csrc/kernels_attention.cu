@@ -9,7 +9,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -59,7 +58,8 @@ __device__ __forceinline__ int32_t token_limit(const AttnArgs& a, int32_t t, int
 // ------------------------------------------------------------------------------------------------ the pass
 
 // Shared memory of a CTA: operand blocks of 64 rows x 64 values (128-byte rows, 128-byte swizzle): the
-// rotated part of the queries, then three stages of keys.
+// rotated part of the queries, then three stages of keys.  A tile's weights take the place of its keys' rotated
+// part, which only the first product reads.
 constexpr uint32_t kBlock = 64 * 128;
 constexpr int kLatentBlocks = kLatentDim / 64;               // 8; the rotated part is a ninth
 constexpr int kHalf = kLatentBlocks / 2;                     // blocks per half: values 0 .. 255, 256 .. 511
@@ -67,17 +67,17 @@ constexpr uint32_t kStage = (kLatentBlocks + 1) * kBlock;
 constexpr uint32_t kRotated = kLatentBlocks * kBlock;        // within a stage
 constexpr int kStages = 3;
 constexpr uint32_t kOffK = kBlock;
-constexpr uint32_t kSmemBytes = kOffK + kStages * kStage + 1024;   // 1024: the blocks' alignment
+constexpr uint32_t kSmemBytes = kOffK + kStages * kStage;
 // the result on its way out, over the keys' stages: rows of 512 fp32 or bf16 values, padded to spread the banks
 constexpr uint32_t kOutRow32 = kLatentDim * 4 + 16, kOutRow16 = kLatentDim * 2 + 16;
 static_assert(64 * kOutRow32 <= kStages * kStage, "the result must fit");
 
 // Tensor memory.  A 64-row accumulator fills 16 of every 32 lanes, and a product's A operand in tensor memory
 // sits in the lanes of its result, so the values 0 .. 255 live in the lower 16 lanes and 256 .. 511 in
-// the upper 16: the queries (128 columns of bf16 pairs), the scores of either half of the values (64
-// columns, summed when they are read), the weights over the scores that they came from (once for each half),
-// and the output (256 columns).  Keeping queries and weights here leaves the shared memory's bandwidth, which
-// bounds a 64-row product with both operands in it, to the keys, and its room to a third stage.
+// the upper 16: the queries (128 columns of bf16 pairs), two tiles of scores (64 columns each, one sum for
+// either half of the values, added when they are read) and the output (256 columns).  Keeping the queries here
+// leaves the shared memory's bandwidth, which bounds a 64 x 64 product with both operands in it, to the
+// keys, and its room to a third stage.
 // All 512 columns are taken, so the allocation starts at column 0, a constant for the issuing thread.
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 0;
@@ -86,9 +86,10 @@ constexpr uint32_t kTmemQ = 384;
 constexpr uint32_t kUpperLanes = 16u << 16;
 
 constexpr int kSoftmaxWarps = 4;
-constexpr int kMmaWarp = 4;
+constexpr int kFirstWarp = 4, kSecondWarp = 5;                // issue the first and the second products
+constexpr int kLoadWarp0 = 6;
 constexpr int kLoadWarps = 8;
-constexpr int kThreads = (kSoftmaxWarps + 1 + kLoadWarps) * 32;
+constexpr int kThreads = (kLoadWarp0 + kLoadWarps) * 32;
 
 // The running maximum may lag behind the true one by this much (base 2) before the sums are rescaled:
 // fp32 sums and bf16 weights lose nothing by weights of up to 2^8.
@@ -105,21 +106,39 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Two E4M3 codes (the low 16 bits) times a power of two, exact in bf16.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes, float scale) {
-  uint32_t h;
-  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(h) : "r"(codes));
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  return bf16x2(f.x * scale, f.y * scale);
+// Four E4M3 codes times a power of two, exact in bf16 (out[0]: codes 0 and 1).  Moved to the place of bf16's low
+// exponent bits a code reads as its value times 2^-120, subnormals too; one product with 2^120 * scale (f, a bf16
+// pair) puts that right.  Two instructions a value beside it; the converting instruction took 2.5 times as long.
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t codes, __nv_bfloat162 f, uint32_t (&out)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t t = __byte_perm(codes, 0u, i == 0 ? 0x1404 : 0x3424);       // a code in the upper byte of each half
+    const uint32_t b = (t & 0x80008000u) | ((t >> 4) & 0x07F007F0u);
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), f);
+    out[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+// The same for any scale and for NaN codes.
+__device__ __noinline__ void e4m3x4_to_bf16_any(uint32_t codes, float scale, uint32_t (&out)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t h;
+    asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(h) : "r"(codes >> (16 * i)));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    out[i] = bf16x2(f.x * scale, f.y * scale);
+  }
 }
 
 struct __align__(8) Shared {
   uint64_t full[kStages][2];    // a half of a tile's keys is in shared memory (the second half with the rotated part)
+  uint64_t listed[kStages];     // `valid` of a tile is written
   uint64_t empty[kStages][2];   // a half of the tile's second product is done
   uint64_t scores[2];           // a score tile is complete
-  uint64_t weights[2];          // the weights of a tile are in tensor memory, the output is rescaled
+  uint64_t taken[2];            // and read
+  uint64_t weights[2];          // the weights of a tile are in shared memory, the output is rescaled
   uint64_t queries;             // the queries are in tensor memory
-  uint64_t drained;             // every product of the CTA is done
+  uint64_t drained[2];          // every first, every second product of the CTA is done
   uint32_t tmem;
   int abort;
   int32_t key_end;
@@ -129,31 +148,34 @@ struct __align__(8) Shared {
 
 // One CTA per work item: 64 rows against the keys [k0, key_end) in tiles of 64.
 //   8 warps bring each key's row into shared memory (gathered by 16-byte copies; FP8 rows are expanded to
-//   bf16 on the way), one thread issues the products S = Q K^T (64 x 64 x 576) and O += P V (64 x 512 x 64;
-//   V is the same tile read with its values contiguous), 4 warps turn S into weights P.
-// Products are issued in the order in which their operands come: the first of tile i + 1 runs while
-// the weights of tile i are made.  Tiles go in and out in halves of 256 values, so that the loads
-// of one half run under the products of the other.
+//   bf16 on the way), one thread each issues the products S = Q K^T (64 x 64 x 576) and O += P V (64 x 512
+//   x 64; V is the same tile read with its values contiguous), 4 warps turn S into weights P.
+// The scores of tile i + 1 are computed while the weights of tile i are made.  Tiles go in and out in halves
+// of 256 values, so that the loads of one half run under the products of the other.
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, AttnPlan p) {
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  if (warp == kMmaWarp) {
+  const uint32_t smem = smem_addr(smem_raw);             // a constant, and the operands' addresses with it
+  if (warp == kFirstWarp) {
     if (lane == 0) {
       for (int i = 0; i < kStages; ++i) {
         for (int h = 0; h < 2; ++h) {
-          mbar_init(&sh.full[i][h], kLoadWarps);
+          // each loading thread once for its stores (FP8) and once for its copies
+          mbar_init(&sh.full[i][h], kLoadWarps * 32 * (FP8 && h == 1 ? 2 : 1));
           mbar_init(&sh.empty[i][h], 1);
         }
+        mbar_init(&sh.listed[i], kLoadWarps);
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&sh.scores[i], 1);
+        mbar_init(&sh.taken[i], kSoftmaxWarps);
         mbar_init(&sh.weights[i], kSoftmaxWarps);
       }
       mbar_init(&sh.queries, kSoftmaxWarps);
-      mbar_init(&sh.drained, 1);
+      mbar_init(&sh.drained[0], 1);
+      mbar_init(&sh.drained[1], 1);
       sh.abort = 0;
       sh.key_end = 0;
       fence_barrier_init();
@@ -190,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
     slot += p.shared_slots;
   }
   const int32_t* idx = a.idx ? a.idx + static_cast<int64_t>(token) * a.top_k : nullptr;
-  const int lw = warp - kMmaWarp - 1;                    // loads: rows 8 lw .. 8 lw + 7 of every block
+  const int lw = warp - kLoadWarp0;                      // loads: rows 8 lw .. 8 lw + 7 of every block
   const int sub = lane >> 3, col = lane & 7;             // a lane's 16-byte column, rows sub and sub + 4
   if (lw >= 0 && a.kv.rope) {
 #pragma unroll
@@ -242,11 +264,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
 
   if (lw >= 0) {
     // ---------------------------------------------------------------- loads
-    auto arrive = [&](int i, int h) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.full[i % kStages][h]);
-    };
     // This warp's key `col` of a tile, the same in the lanes of one column: its position (-1: none) is read three
     // tiles ahead, its page two, so that neither load is waited for.
     auto position = [&](int i) -> int32_t {
@@ -270,20 +287,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
         for (int h = 0; h < 2; ++h) codes[h][j] = rj >= 0 ? __ldg(src + 16 * h) : make_uint4(0u, 0u, 0u, 0u);
       }
     };
-    // Tiles under way are handed to the products when the warp would wait otherwise, oldest first.  Each has two
-    // groups of copies, one per half; an FP8 tile's first half has none and was handed over when it was written.
-    int landed = 0, issued = 0;
-    auto hand_over = [&] {
-      for (; landed < issued; ++landed) {
-        const int behind = issued - landed - 1;          // tiles issued after this one: fewer than the stages
-        if constexpr (!FP8) {
-          if (behind == 0) cp_async_wait<1>(); else if (behind == 1) cp_async_wait<3>(); else cp_async_wait<5>();
-          arrive(landed, 0);
-        }
-        if (behind == 0) cp_async_wait<0>(); else if (behind == 1) cp_async_wait<2>(); else cp_async_wait<4>();
-        arrive(landed, 1);
-      }
-    };
     const int32_t pos0 = position(0), pos1 = position(1);
     int32_t pos2 = position(2), pos3 = position(3);
     const int32_t page0 = page_of(pos0), page1 = page_of(pos1);
@@ -298,22 +301,35 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       const uint32_t valid = __ballot_sync(0xffffffffu, row >= 0) & 0xFFu;
       uint32_t wide[2][4][8];                            // the codes' values in bf16
       if constexpr (FP8) {
+        uint32_t odd = scale > 128.f || !(scale >= 0x1p-100f || scale == 0.f);   // 2^120 * scale must be an ordinary bf16
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t w[4] = {codes[h][j].x, codes[h][j].y, codes[h][j].z, codes[h][j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) odd |= ((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // a NaN code
+          }
+        const bool plain = !__any_sync(0xffffffffu, odd != 0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float s = __shfl_sync(0xffffffffu, scale, 2 * j + (lane >> 4));
+          const __nv_bfloat162 f = __float2bfloat162_rn(s * 0x1p120f);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t w[4] = {codes[h][j].x, codes[h][j].y, codes[h][j].z, codes[h][j].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              wide[h][j][2 * e] = e4m3x2_to_bf16x2(w[e] & 0xFFFFu, s);
-              wide[h][j][2 * e + 1] = e4m3x2_to_bf16x2(w[e] >> 16, s);
+              uint32_t out[2];
+              if (plain) e4m3x4_to_bf16(w[e], f, out);
+              else e4m3x4_to_bf16_any(w[e], s, out);
+              wide[h][j][2 * e] = out[0];
+              wide[h][j][2 * e + 1] = out[1];
             }
           }
         }
       }
       if constexpr (FP8) fetch(next);                    // before the wait for this tile's place
-      if (i >= kStages && !__all_sync(0xffffffffu, mbar_test(&sh.empty[st][0], parity))) hand_over();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (i >= kStages) {
@@ -321,7 +337,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
           ok = __all_sync(0xffffffffu, ok);              // a warp leaves as one
           if (!ok) break;
         }
-        if (h == 1 && lane == 0) sh.valid[st][lw] = static_cast<uint8_t>(valid);
+        if (h == 1 && lane == 0) {
+          sh.valid[st][lw] = static_cast<uint8_t>(valid);
+          mbar_arrive(&sh.listed[st]);
+        }
         if constexpr (!FP8) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
@@ -342,7 +361,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
                        static_cast<const __nv_bfloat16*>(a.kv.rope) + static_cast<int64_t>(max(rj, 0)) * kLatentRope + col * 8, rj >= 0);
           }
         }
-        cp_async_commit();
         if constexpr (FP8) {
           // two 16-byte columns of block (lane % 16) / 4.  Lanes of odd blocks store the second one first, so that
           // the eight lanes of a store's phase fall on different banks.
@@ -361,103 +379,90 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
                            : "memory");
             }
           }
-          if (h == 0) arrive(i, 0);
+          fence_proxy_async_smem();
+          mbar_arrive(&sh.full[st][h]);
         }
+        if (!FP8 || h == 1) cp_async_arrive(&sh.full[st][h]);   // when this thread's copies so far have landed
       }
       if (!ok) break;
-      ++issued;
       row = next;
       next = row_of(pos2, page2);
       page2 = page_of(pos3);
       pos2 = pos3;
       pos3 = position(i + 4);
     }
-    if (ok) hand_over();
-    cp_async_wait<0>();
-  } else if (warp == kMmaWarp) {
-    // ---------------------------------------------------------------- products
+    cp_async_wait_all();
+  } else if (warp == kFirstWarp) {
+    // ---------------------------------------------------------------- scores = Q K^T
+    // Two warps issue, one per product: the tensor cores take either's next while the other's issuer waits or
+    // reads a barrier (300 cycles between two batches of one issuer stood idle otherwise).
     if (elect_one()) {
-      constexpr uint32_t idesc_s = make_idesc(1, kAttnRows, kAttnTile);
-      constexpr uint32_t idesc_o = make_idesc(1, kAttnRows, 256) | kIdescBMnMajor;
-      int q = 0, v = 0;                                  // next tiles of the first and of the second product
-      int half = 0;                                      // halves of tile q's first product already issued
-      // scores (+)= Q K[st]^T over one half of the values (the second with the rotated part), the stage a constant
-      auto first = [&](auto st, auto h, uint32_t d) {
-        constexpr uint32_t stage = kOffK + decltype(st)::value * kStage;
-        constexpr int upper = decltype(h)::value;
+      constexpr uint32_t idesc = make_idesc(1, kAttnRows, kAttnTile);
+      bool ok = tiles == 0 || mbar_wait(&sh.queries, 0, &sh.abort);
+      int st = 0;
+      uint32_t phase = 0;
+      for (int i = 0; i < tiles && ok; ++i) {
+        const uint32_t stage = smem + kOffK + st * kStage;
+        const uint32_t d = kTmemS + (i & 1) * kAttnTile;
+        if (i >= 2) ok = mbar_wait(&sh.taken[i & 1], ((i >> 1) - 1) & 1, &sh.abort);
+        ok = ok && mbar_wait(&sh.full[st][0], phase, &sh.abort);
+        if (!ok) break;
+        fence_proxy_async_smem();                        // the copies that the barrier reported
+        tc_fence_after();
 #pragma unroll
         for (int c = 0; c < kHalf; ++c)
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            umma_f16_ts(d + upper * kUpperLanes, kTmemQ + (c * 4 + ks) * 8 + upper * kUpperLanes,
-                        sdesc_kmajor_sw128(smem + stage + (upper * kHalf + c) * kBlock + ks * 32), idesc_s, c > 0 || ks > 0);
-        if constexpr (upper) {
-          if (a.kv.rope) {
+            umma_f16_ts(d, kTmemQ + (c * 4 + ks) * 8, sdesc_kmajor_sw128(stage + c * kBlock + ks * 32), idesc, c > 0 || ks > 0);
+        ok = mbar_wait(&sh.full[st][1], phase, &sh.abort);
+        if (!ok) break;
+        fence_proxy_async_smem();
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_f16(d + kUpperLanes, sdesc_kmajor_sw128(smem + ks * 32),
-                       sdesc_kmajor_sw128(smem + stage + kRotated + ks * 32), idesc_s, 1);
-          }
+        for (int c = 0; c < kHalf; ++c)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_f16_ts(d + kUpperLanes, kTmemQ + (c * 4 + ks) * 8 + kUpperLanes,
+                        sdesc_kmajor_sw128(stage + (kHalf + c) * kBlock + ks * 32), idesc, c > 0 || ks > 0);
+        if (a.kv.rope) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_f16(d + kUpperLanes, sdesc_kmajor_sw128(smem + ks * 32), sdesc_kmajor_sw128(stage + kRotated + ks * 32), idesc, 1);
         }
-      };
-      auto second = [&](auto st, uint32_t w, uint32_t accumulate) {
-        constexpr uint32_t stage = kOffK + decltype(st)::value * kStage;
+        umma_commit(&sh.scores[i & 1]);
+        if (++st == kStages) {
+          st = 0;
+          phase ^= 1;
+        }
+      }
+      umma_commit(&sh.drained[0]);
+      int alone = 0;                                     // also after an abort: nothing may run on freed tensor memory
+      mbar_wait(&sh.drained[0], 0, &alone);
+    }
+    __syncwarp();
+  } else if (warp == kSecondWarp) {
+    // ---------------------------------------------------------------- output += P V
+    if (elect_one()) {
+      constexpr uint32_t idesc = make_idesc(1, kAttnRows, 256) | kIdescBMnMajor;
+      int st = 0;
+      for (int i = 0; i < tiles; ++i) {
+        // the weights came from scores of the same keys, so those are in shared memory
+        if (!mbar_wait(&sh.weights[i & 1], (i >> 1) & 1, &sh.abort)) break;
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint32_t stage = smem + kOffK + st * kStage;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
           for (int ks = 0; ks < kAttnTile / 16; ++ks)
-            umma_f16_ts(kTmemO + h * kUpperLanes, w + ks * 8 + h * kUpperLanes,
-                        sdesc_mnmajor_sw128(smem + stage + h * kHalf * kBlock + ks * 2048, kBlock), idesc_o, ks > 0 ? 1u : accumulate);
-          umma_commit(&sh.empty[decltype(st)::value][h]);
+            umma_f16(kTmemO + h * kUpperLanes, sdesc_kmajor_sw128(stage + kRotated + ks * 32),
+                     sdesc_mnmajor_sw128(stage + h * kHalf * kBlock + ks * 2048, kBlock), idesc, i > 0 || ks > 0);
+          umma_commit(&sh.empty[st][h]);
         }
-      };
-      constexpr std::integral_constant<int, 0> c0{};
-      constexpr std::integral_constant<int, 1> c1{};
-      constexpr std::integral_constant<int, 2> c2{};
-      int qs = 0, vs = 0;                                // their stages
-      uint32_t q_phase = 0;
-      if (tiles > 0) {
-        int* abort = &sh.abort;
-        mbar_wait(&sh.queries, 0, abort);
-        tc_fence_after();
+        if (++st == kStages) st = 0;
       }
-      long long since = clock64();
-      while (v < tiles) {
-        // a score tile is free once the second product of the tile before last, which reads its weights there, is issued
-        if (q < tiles && q - v < 2 && mbar_test(&sh.full[qs][half], q_phase)) {
-          tc_fence_after();
-          const uint32_t d = kTmemS + (q & 1) * kAttnTile;
-          if (half == 0) {
-            if (qs == 0) first(c0, c0, d); else if (qs == 1) first(c1, c0, d); else first(c2, c0, d);
-            half = 1;
-          } else {
-            if (qs == 0) first(c0, c1, d); else if (qs == 1) first(c1, c1, d); else first(c2, c1, d);
-            umma_commit(&sh.scores[q & 1]);
-            half = 0;
-            ++q;
-            if (++qs == kStages) {
-              qs = 0;
-              q_phase ^= 1;
-            }
-          }
-          since = clock64();
-        } else if (v < q && mbar_test(&sh.weights[v & 1], (v >> 1) & 1)) {
-          tc_fence_after();
-          const uint32_t w = kTmemS + (v & 1) * kAttnTile;
-          if (vs == 0) second(c0, w, v > 0); else if (vs == 1) second(c1, w, 1u); else second(c2, w, 1u);
-          if (++vs == kStages) vs = 0;
-          ++v;
-          since = clock64();
-        } else if (*const_cast<volatile int*>(&sh.abort)) {
-          break;
-        } else if (clock64() - since > kWaitLimitCycles) {
-          *const_cast<volatile int*>(&sh.abort) = 1;
-          break;
-        }
-      }
-      umma_commit(&sh.drained);
-      int alone = 0;                                     // also after an abort: nothing may run on freed tensor memory
-      mbar_wait(&sh.drained, 0, &alone);
+      umma_commit(&sh.drained[1]);
+      int alone = 0;
+      mbar_wait(&sh.drained[1], 0, &alone);
     }
     __syncwarp();
   } else {
@@ -496,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
     }
     for (int i = 0; i < tiles; ++i) {
       ok = mbar_wait<true>(&sh.scores[i & 1], (i >> 1) & 1, &sh.abort);
-      ok = ok && mbar_wait<true>(&sh.full[i % kStages][1], (i / kStages) & 1, &sh.abort);   // for `valid`
+      ok = ok && mbar_wait<true>(&sh.listed[i % kStages], (i / kStages) & 1, &sh.abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -506,6 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       tmem_ld_16x256b_x8(tile + kUpperLanes, raw2);
       const uint64_t present = *reinterpret_cast<const uint64_t*>(sh.valid[i % kStages]);
       tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.taken[i & 1]);
       float x[2][16];
       const int32_t kb = k0 + i * kAttnTile;
       uint64_t mask[2];
@@ -552,19 +560,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
           m[r] = mn;
         }
       }
-      uint32_t w[16];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float ref = m[r] == -INFINITY ? 0.f : m[r];
+        const uint32_t dst = smem + kOffK + (i % kStages) * kStage + kRotated + (warp * 16 + fr + 8 * r) * 128 + (lane & 3) * 4;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float lo = exp2_fast(fmaf(x[r][2 * j], a.scale_log2, -ref)), hi = exp2_fast(fmaf(x[r][2 * j + 1], a.scale_log2, -ref));
           l[r] += lo + hi;                               // the sum keeps fp32; the product's operand is bf16
-          w[2 * j + r] = bf16x2(lo, hi);
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + ((j ^ fr) << 4)), "r"(bf16x2(lo, hi)) : "memory");
         }
       }
-      tmem_st_16x128b_x8(tile, w);
-      tmem_st_16x128b_x8(tile + kUpperLanes, w);
       if (rescale && i > 0) {
         // the output of the tiles before this one, complete, times the factor
         ok = mbar_wait<true>(&sh.empty[(i - 1) % kStages][1], ((i - 1) / kStages) & 1, &sh.abort);
@@ -584,8 +590,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
           tmem_st_32x32b_x32(quadrant + kTmemO + c, o);
         }
+        tmem_st_wait();
       }
-      tmem_st_wait();
+      fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.weights[i & 1]);
@@ -664,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
   if (*const_cast<volatile int*>(&sh.abort) && lane == 0) record_error(a.err, DSA_DEVERR_TIMEOUT, static_cast<int>(blockIdx.x));
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == kFirstWarp) {
     tc_fence_after();
     tmem_dealloc(sh.tmem, kTmemCols);
   }
