@@ -106,10 +106,11 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Four E4M3 codes times a power of two, exact in bf16 (out[0]: codes 0 and 1).  Moved to the place of bf16's low
+// Four E4M3 codes times a power of two, exact in bf16 (x: codes 0 and 1).  Moved to the place of bf16's low
 // exponent bits a code reads as its value times 2^-120, subnormals too; one product with 2^120 * scale (f, a bf16
-// pair) puts that right.  Two instructions a value beside it; the converting instruction took 2.5 times as long.
-__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t codes, __nv_bfloat162 f, uint32_t (&out)[2]) {
+// pair) puts that right.
+__device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t codes, __nv_bfloat162 f) {
+  uint32_t out[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint32_t t = __byte_perm(codes, 0u, i == 0 ? 0x1404 : 0x3424);       // a code in the upper byte of each half
@@ -117,17 +118,20 @@ __device__ __forceinline__ void e4m3x4_to_bf16(uint32_t codes, __nv_bfloat162 f,
     const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), f);
     out[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
+  return make_uint2(out[0], out[1]);
 }
 
 // The same for any scale and for NaN codes.
-__device__ __noinline__ void e4m3x4_to_bf16_any(uint32_t codes, float scale, uint32_t (&out)[2]) {
+__device__ __noinline__ uint2 e4m3x4_to_bf16_any(uint32_t codes, float scale) {
+  uint32_t out[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     uint32_t h;
-    asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(h) : "r"(codes >> (16 * i)));
+    asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(h) : "r"((codes >> (16 * i)) & 0xFFFFu));
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
     out[i] = bf16x2(f.x * scale, f.y * scale);
   }
+  return make_uint2(out[0], out[1]);
 }
 
 struct __align__(8) Shared {
@@ -311,20 +315,34 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
             for (int e = 0; e < 4; ++e) odd |= ((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // a NaN code
           }
         const bool plain = !__any_sync(0xffffffffu, odd != 0);
+        if (plain) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float s = __shfl_sync(0xffffffffu, scale, 2 * j + (lane >> 4));
-          const __nv_bfloat162 f = __float2bfloat162_rn(s * 0x1p120f);
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 f = __float2bfloat162_rn(__shfl_sync(0xffffffffu, scale, 2 * j + (lane >> 4)) * 0x1p120f);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t w[4] = {codes[h][j].x, codes[h][j].y, codes[h][j].z, codes[h][j].w};
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t w[4] = {codes[h][j].x, codes[h][j].y, codes[h][j].z, codes[h][j].w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t out[2];
-              if (plain) e4m3x4_to_bf16(w[e], f, out);
-              else e4m3x4_to_bf16_any(w[e], s, out);
-              wide[h][j][2 * e] = out[0];
-              wide[h][j][2 * e + 1] = out[1];
+              for (int e = 0; e < 4; ++e) {
+                const uint2 v = e4m3x4_to_bf16(w[e], f);
+                wide[h][j][2 * e] = v.x;
+                wide[h][j][2 * e + 1] = v.y;
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float s = __shfl_sync(0xffffffffu, scale, 2 * j + (lane >> 4));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t w[4] = {codes[h][j].x, codes[h][j].y, codes[h][j].z, codes[h][j].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint2 v = e4m3x4_to_bf16_any(w[e], s);
+                wide[h][j][2 * e] = v.x;
+                wide[h][j][2 * e + 1] = v.y;
+              }
             }
           }
         }
