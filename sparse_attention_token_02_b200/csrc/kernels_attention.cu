@@ -106,32 +106,14 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Four E4M3 codes times a power of two, exact in bf16 (x: codes 0 and 1).  Moved to the place of bf16's low
-// exponent bits a code reads as its value times 2^-120, subnormals too; one product with 2^120 * scale (f, a bf16
-// pair) puts that right.
-__device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t codes, __nv_bfloat162 f) {
-  uint32_t out[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t t = __byte_perm(codes, 0u, i == 0 ? 0x1404 : 0x3424);       // a code in the upper byte of each half
-    const uint32_t b = (t & 0x80008000u) | ((t >> 4) & 0x07F007F0u);
-    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), f);
-    out[i] = *reinterpret_cast<const uint32_t*>(&v);
-  }
-  return make_uint2(out[0], out[1]);
-}
-
-// The same for any scale and for NaN codes.
-__device__ __noinline__ uint2 e4m3x4_to_bf16_any(uint32_t codes, float scale) {
-  uint32_t out[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t h;
-    asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(h) : "r"((codes >> (16 * i)) & 0xFFFFu));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    out[i] = bf16x2(f.x * scale, f.y * scale);
-  }
-  return make_uint2(out[0], out[1]);
+// Two E4M3 codes (the low 16 bits) times a power of two, exact in bf16.  The two conversions and the products
+// spread over the ALU and FMA pipes; moving the bits by hand (a byte permutation, a shift, two logic instructions
+// and one product for a pair, and a look for NaN codes) kept the ALU pipe busy for longer.
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes, float scale) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(h) : "r"(codes));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return bf16x2(f.x * scale, f.y * scale);
 }
 
 struct __align__(8) Shared {
@@ -278,15 +260,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
     auto row_of = [&](int32_t pos, int32_t page) -> int32_t {
       return pos < 0 ? -1 : page_row(a.kv, page, pos, a.err, token < 0 ? row0 / a.H : token);
     };
-    // 16 FP8 codes of each half of four of the warp's rows: row 2 j + lane / 16, codes from 16 (lane % 16)
+    // 16 FP8 codes of each half of four of the warp's rows: row 2 j + pair, codes from 16 vec.  Eight neighbouring lanes
+    // hold four neighbouring vectors of an even and of an odd row, whose places fall on different banks.
+    const int pair = (lane >> 2) & 1, vec = (lane & 3) + 4 * (lane >> 3);
     uint4 codes[2][4];
     float scale = 0.f;
     auto fetch = [&](int32_t row) {
-      scale = row >= 0 ? a.kv.scale[row] : 0.f;
+      scale = row >= 0 ? __ldg(a.kv.scale + row) : 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int32_t rj = __shfl_sync(0xffffffffu, row, 2 * j + (lane >> 4));
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.kv.latent) + static_cast<int64_t>(rj) * kLatentDim) + (lane & 15);
+        const int32_t rj = __shfl_sync(0xffffffffu, row, 2 * j + pair);
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.kv.latent) + static_cast<int64_t>(rj) * kLatentDim) + vec;
 #pragma unroll
         for (int h = 0; h < 2; ++h) codes[h][j] = rj >= 0 ? __ldg(src + 16 * h) : make_uint4(0u, 0u, 0u, 0u);
       }
@@ -305,44 +289,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       const uint32_t valid = __ballot_sync(0xffffffffu, row >= 0) & 0xFFu;
       uint32_t wide[2][4][8];                            // the codes' values in bf16
       if constexpr (FP8) {
-        uint32_t odd = scale > 128.f || !(scale >= 0x1p-100f || scale == 0.f);   // 2^120 * scale must be an ordinary bf16
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 4; ++j) {
+          const float s = __shfl_sync(0xffffffffu, scale, 2 * j + pair);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t w[4] = {codes[h][j].x, codes[h][j].y, codes[h][j].z, codes[h][j].w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) odd |= ((w[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // a NaN code
-          }
-        const bool plain = !__any_sync(0xffffffffu, odd != 0);
-        if (plain) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 f = __float2bfloat162_rn(__shfl_sync(0xffffffffu, scale, 2 * j + (lane >> 4)) * 0x1p120f);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t w[4] = {codes[h][j].x, codes[h][j].y, codes[h][j].z, codes[h][j].w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint2 v = e4m3x4_to_bf16(w[e], f);
-                wide[h][j][2 * e] = v.x;
-                wide[h][j][2 * e + 1] = v.y;
-              }
-            }
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float s = __shfl_sync(0xffffffffu, scale, 2 * j + (lane >> 4));
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t w[4] = {codes[h][j].x, codes[h][j].y, codes[h][j].z, codes[h][j].w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint2 v = e4m3x4_to_bf16_any(w[e], s);
-                wide[h][j][2 * e] = v.x;
-                wide[h][j][2 * e + 1] = v.y;
-              }
+            for (int e = 0; e < 4; ++e) {
+              wide[h][j][2 * e] = e4m3x2_to_bf16x2(w[e] & 0xFFFFu, s);
+              wide[h][j][2 * e + 1] = e4m3x2_to_bf16x2(w[e] >> 16, s);
             }
           }
         }
@@ -380,22 +336,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
           }
         }
         if constexpr (FP8) {
-          // two 16-byte columns of block (lane % 16) / 4.  Lanes of odd blocks store the second one first, so that
-          // the eight lanes of a store's phase fall on different banks.
-          const int swap = (lane >> 2) & 1;
+          // two 16-byte columns of block vec / 4
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int r8 = 2 * j + (lane >> 4);
+            const int r8 = 2 * j + pair;
             const uint32_t* v = wide[h][j];
-            const uint32_t base = stage + (h * kHalf + ((lane & 15) >> 2)) * kBlock + (lw * 8 + r8) * 128;
+            const uint32_t base = stage + (h * kHalf + (vec >> 2)) * kBlock + (lw * 8 + r8) * 128;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int second = x ^ swap;
-              const uint32_t dst = base + ((((lane & 3) * 2 + second) ^ r8) << 4);
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(second ? v[4] : v[0]), "r"(second ? v[5] : v[1]),
-                           "r"(second ? v[6] : v[2]), "r"(second ? v[7] : v[3])
+            for (int x = 0; x < 2; ++x)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + ((((vec & 3) * 2 + x) ^ r8) << 4)), "r"(v[4 * x]),
+                           "r"(v[4 * x + 1]), "r"(v[4 * x + 2]), "r"(v[4 * x + 3])
                            : "memory");
-            }
           }
           fence_proxy_async_smem();
           mbar_arrive(&sh.full[st][h]);
@@ -416,14 +367,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
     // reads a barrier (300 cycles between two batches of one issuer stood idle otherwise).
     if (elect_one()) {
       constexpr uint32_t idesc = make_idesc(1, kAttnRows, kAttnTile);
-      bool ok = tiles == 0 || mbar_wait(&sh.queries, 0, &sh.abort);
+      bool ok = tiles == 0 || mbar_wait<true>(&sh.queries, 0, &sh.abort);
       int st = 0;
       uint32_t phase = 0;
       for (int i = 0; i < tiles && ok; ++i) {
         const uint32_t stage = smem + kOffK + st * kStage;
         const uint32_t d = kTmemS + (i & 1) * kAttnTile;
-        if (i >= 2) ok = mbar_wait(&sh.taken[i & 1], ((i >> 1) - 1) & 1, &sh.abort);
-        ok = ok && mbar_wait(&sh.full[st][0], phase, &sh.abort);
+        if (i >= 2) ok = mbar_wait<true>(&sh.taken[i & 1], ((i >> 1) - 1) & 1, &sh.abort);
+        ok = ok && mbar_wait<true>(&sh.full[st][0], phase, &sh.abort);
         if (!ok) break;
         fence_proxy_async_smem();                        // the copies that the barrier reported
         tc_fence_after();
@@ -432,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             umma_f16_ts(d, kTmemQ + (c * 4 + ks) * 8, sdesc_kmajor_sw128(stage + c * kBlock + ks * 32), idesc, c > 0 || ks > 0);
-        ok = mbar_wait(&sh.full[st][1], phase, &sh.abort);
+        ok = mbar_wait<true>(&sh.full[st][1], phase, &sh.abort);
         if (!ok) break;
         fence_proxy_async_smem();
 #pragma unroll
@@ -454,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       }
       umma_commit(&sh.drained[0]);
       int alone = 0;                                     // also after an abort: nothing may run on freed tensor memory
-      mbar_wait(&sh.drained[0], 0, &alone);
+      mbar_wait<true>(&sh.drained[0], 0, &alone);
     }
     __syncwarp();
   } else if (warp == kSecondWarp) {
@@ -464,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       int st = 0;
       for (int i = 0; i < tiles; ++i) {
         // the weights came from scores of the same keys, so those are in shared memory
-        if (!mbar_wait(&sh.weights[i & 1], (i >> 1) & 1, &sh.abort)) break;
+        if (!mbar_wait<true>(&sh.weights[i & 1], (i >> 1) & 1, &sh.abort)) break;
         fence_proxy_async_smem();
         tc_fence_after();
         const uint32_t stage = smem + kOffK + st * kStage;
@@ -480,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       }
       umma_commit(&sh.drained[1]);
       int alone = 0;
-      mbar_wait(&sh.drained[1], 0, &alone);
+      mbar_wait<true>(&sh.drained[1], 0, &alone);
     }
     __syncwarp();
   } else {

@@ -21,20 +21,34 @@ namespace {
 
 constexpr int kVec = 8;                       // values per thread and step: 16 bytes of bf16
 
+// Eight values as they lie in memory
 template <bool F32>
-__device__ __forceinline__ void load8(const void* p, int64_t elem, float (&v)[kVec]) {
-  if constexpr (F32) {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + elem);
-    const float4 a = f[0], b = f[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p) + elem);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Raw {
+  uint4 u[F32 ? 2 : 1];
+};
+
+template <bool F32>
+__device__ __forceinline__ Raw<F32> load8(const void* p, int64_t elem) {
+  Raw<F32> r;
+  const uint4* u = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + elem * (F32 ? 4 : 2));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) r.u[i] = u[i];
+  return r;
+}
+
+template <bool F32>
+__device__ __forceinline__ void widen(const Raw<F32>& r, float (&v)[kVec]) {
+#pragma unroll
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+    const uint32_t w[4] = {r.u[i].x, r.u[i].y, r.u[i].z, r.u[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (F32) {
+        v[4 * i + j] = __uint_as_float(w[j]);
+      } else {
+        v[2 * j] = __uint_as_float(w[j] << 16);
+        v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      }
     }
   }
 }
@@ -100,6 +114,16 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
   launch_dependents();
   const int64_t row = blockIdx.x;
   const int nvec = a.d / kVec, tid = threadIdx.x;
+  // every load of the row before the first store, which might be to the same memory
+  Raw<F32> rx[VPT], rr[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = i * blockDim.x + tid;
+    if (v < nvec) {
+      rx[i] = load8<F32>(a.x, row * a.x_stride + v * kVec);
+      if (a.residual) rr[i] = load8<F32>(a.residual, row * a.d + v * kVec);
+    }
+  }
   float s[VPT][kVec];
   float sq = 0.f;
 #pragma unroll
@@ -108,10 +132,10 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
 #pragma unroll
     for (int e = 0; e < kVec; ++e) s[i][e] = 0.f;
     if (v < nvec) {
-      load8<F32>(a.x, row * a.x_stride + v * kVec, s[i]);
+      widen<F32>(rx[i], s[i]);
       if (a.residual) {
         float r[kVec];
-        load8<F32>(a.residual, row * a.d + v * kVec, r);
+        widen<F32>(rr[i], r);
 #pragma unroll
         for (int e = 0; e < kVec; ++e) s[i][e] += r[e];
         store8<F32>(a.residual_out, row * a.d + v * kVec, s[i]);
@@ -128,8 +152,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
     float group_max = 0.f;
     if (v < nvec) {
       float w[kVec];
-      if (a.w_f32) load8<true>(a.weight, v * kVec, w);
-      else load8<false>(a.weight, v * kVec, w);
+      if (a.w_f32) widen<true>(load8<true>(a.weight, v * kVec), w);
+      else widen<false>(load8<false>(a.weight, v * kVec), w);
 #pragma unroll
       for (int e = 0; e < kVec; ++e) {
         s[i][e] = s[i][e] * inv * w[e];
