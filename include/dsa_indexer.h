@@ -488,9 +488,10 @@ DSA_API dsa_status_t dsa_prefix_attention(const dsa_latent_query_t* q, const dsa
                                           int32_t max_keys, float sm_scale, void* out, float* lse, void* workspace,
                                           size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of the two attention calls on the current device (0: none needed). */
+/* Workspace bytes of the two attention calls on the current device (0: none needed); dtype: the cache's. */
 DSA_API size_t dsa_sparse_attention_workspace_bytes(int32_t T, int32_t H, int32_t top_k);
-DSA_API size_t dsa_prefix_attention_workspace_bytes(int32_t T, int32_t H, int32_t prefix_len, int32_t max_keys);
+DSA_API size_t dsa_prefix_attention_workspace_bytes(int32_t T, int32_t H, int32_t prefix_len, int32_t max_keys,
+                                                    dsa_dtype_t dtype);
 
 /* Workspace bytes a call with this batch needs (scores plus scheduling tables). */
 DSA_API size_t dsa_indexer_workspace_bytes(const dsa_query_t* q, const dsa_batch_t* batch, int32_t top_k);

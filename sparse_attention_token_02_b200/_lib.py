@@ -153,7 +153,7 @@ def load() -> ctypes.CDLL:
     lib.dsa_prefix_attention.restype = st
     lib.dsa_sparse_attention_workspace_bytes.argtypes = [I32, I32, I32]
     lib.dsa_sparse_attention_workspace_bytes.restype = ctypes.c_size_t
-    lib.dsa_prefix_attention_workspace_bytes.argtypes = [I32, I32, I32, I32]
+    lib.dsa_prefix_attention_workspace_bytes.argtypes = [I32, I32, I32, I32, ctypes.c_int]
     lib.dsa_prefix_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.dsa_indexer_scores.argtypes = [P(Query), P(KCache), V, P(Batch), V, I64, V]
     lib.dsa_indexer_scores.restype = st

@@ -602,7 +602,8 @@ def dsa_prefix_attention(q_latent, q_rope, cache: LatentCache, page_table, seq_i
     if max_keys is None:
         max_keys = table.max_pages * cache.page_size
     lib = _lib.load()
-    need = lib.dsa_prefix_attention_workspace_bytes(T, H, prefix_len, max_keys) if workspace is None else 0
+    need = 0 if workspace is not None else lib.dsa_prefix_attention_workspace_bytes(
+        T, H, prefix_len, max_keys, DSA_BF16 if cache.latent.dtype is torch.bfloat16 else DSA_FP8_E4M3)
     out, lse, workspace, given = _outputs(T, H, q_latent, out, lse, workspace, need)
     _one_device(q_latent, cache.latent, cache.rope, cache.scale, page_table, seq_ids, key_lens, out, lse, workspace)
     _one_device(q_latent, q_rope, contiguous=False)
@@ -616,8 +617,9 @@ def dsa_sparse_attention_workspace_bytes(T: int, H: int, top_k: int) -> int:
     return int(_lib.load().dsa_sparse_attention_workspace_bytes(T, H, top_k))
 
 
-def dsa_prefix_attention_workspace_bytes(T: int, H: int, prefix_len: int, max_keys: int) -> int:
-    return int(_lib.load().dsa_prefix_attention_workspace_bytes(T, H, prefix_len, max_keys))
+def dsa_prefix_attention_workspace_bytes(T: int, H: int, prefix_len: int, max_keys: int, fp8: bool = False) -> int:
+    return int(_lib.load().dsa_prefix_attention_workspace_bytes(T, H, prefix_len, max_keys,
+                                                                DSA_FP8_E4M3 if fp8 else DSA_BF16))
 
 
 def dsa_indexer_scores(q, cache: IndexerKCache, w, seq_lens, q_scale=None, q_lens=None, k_base=None, ld=None,

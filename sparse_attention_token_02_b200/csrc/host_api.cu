@@ -1312,7 +1312,7 @@ dsa_status_t check_latent(const dsa_latent_cache_t* c, const dsa_page_table_t* t
   if (t->num_seqs < 1 || t->max_pages < 1) return fail(DSA_ERR_INVALID_ARG, "page table must have at least one row and one column");
   if (!aligned16(c->latent) || !aligned16(c->rope)) return fail(DSA_ERR_INVALID_ARG, "latent and rope must be 16-byte aligned");
   *v = LatentView{c->latent, c->dtype == DSA_FP8_E4M3 ? c->scale : nullptr, c->d_r ? c->rope : nullptr, c->num_pages,
-                  c->page_size, c->dtype == DSA_FP8_E4M3, t->pages, t->num_seqs, t->max_pages};
+                  c->page_size, c->page_size & (c->page_size - 1) ? -1 : __builtin_ctz(c->page_size), c->dtype == DSA_FP8_E4M3, t->pages, t->num_seqs, t->max_pages};
   return DSA_OK;
 }
 
@@ -1397,11 +1397,9 @@ dsa_status_t run_attention(const dsa_latent_query_t* q, AttnArgs* a, int64_t sha
   Ctx* c = nullptr;
   dsa_status_t st = get_ctx(stream, &c);
   if (st != DSA_OK) return st;
-  const AttnPlan p = plan_attention(q->T, q->H, shared_keys, own_keys, current_sms());
-  void* ws = nullptr;
-  if ((st = attention_parts(c, attention_workspace(p, q->T, q->H), workspace, workspace_bytes, &ws)) != DSA_OK) return st;
-  a->part_o = static_cast<float*>(ws);
-  a->part_lse = a->part_o ? a->part_o + size_t(p.slots()) * q->T * q->H * kLatentDim : nullptr;
+  const AttnPlan p = plan_attention(q->T, q->H, shared_keys, own_keys, a->kv.fp8, current_sms());
+  if ((st = attention_parts(c, attention_workspace(p, q->T, q->H, shared_keys), workspace, workspace_bytes, &a->workspace)) != DSA_OK)
+    return st;
   a->err = c->d_err;
   int launched = 0;
   const cudaError_t e = launch_attention(*a, p, &launched, stream);
@@ -1538,12 +1536,12 @@ dsa_status_t dsa_prefix_attention(const dsa_latent_query_t* q, const dsa_latent_
 
 size_t dsa_sparse_attention_workspace_bytes(int32_t T, int32_t H, int32_t top_k) {
   if (T < 1 || H < 1 || H > 128 || top_k < 1 || top_k > kMaxKeys) return 0;
-  return attention_workspace(plan_attention(T, H, 0, top_k, current_sms()), T, H);
+  return attention_workspace(plan_attention(T, H, 0, top_k, false, current_sms()), T, H, 0);
 }
 
-size_t dsa_prefix_attention_workspace_bytes(int32_t T, int32_t H, int32_t prefix_len, int32_t max_keys) {
+size_t dsa_prefix_attention_workspace_bytes(int32_t T, int32_t H, int32_t prefix_len, int32_t max_keys, dsa_dtype_t dtype) {
   if (T < 1 || H < 1 || H > 128 || prefix_len < 0 || max_keys < prefix_len || max_keys > kMaxKeys) return 0;
-  return attention_workspace(plan_attention(T, H, prefix_len, max_keys - prefix_len, current_sms()), T, H);
+  return attention_workspace(plan_attention(T, H, prefix_len, max_keys - prefix_len, dtype == DSA_FP8_E4M3, current_sms()), T, H, prefix_len);
 }
 
 }  // extern "C"

@@ -189,6 +189,7 @@ struct LatentView {
   float* scale;                // [num_pages * page_size] (FP8)
   void* rope;                  // [num_pages * page_size, 64] bf16, or nullptr
   int32_t num_pages, page_size;
+  int32_t page_shift;          // log2(page_size), or -1
   int32_t fp8;
   const int32_t* pages;        // [num_seqs, max_pages]
   int32_t num_seqs, max_pages;
@@ -216,6 +217,7 @@ constexpr int kAttnTile = 64;          // keys per tile; chunks are whole tiles
 struct AttnPlan {
   int32_t shared_groups, shared_slots, shared_chunk;
   int32_t own_groups, own_slots, own_chunk;       // own_groups: row groups of one token
+  int32_t expand;                                 // the shared prefix of an FP8 cache goes to bf16 first
   __host__ __device__ int32_t slots() const { return shared_slots + own_slots; }
 };
 struct AttnArgs {
@@ -225,6 +227,7 @@ struct AttnArgs {
   const void* q_rope;
   int64_t qr_t, qr_h;
   int32_t T, H;
+  LatentView shared;           // the cache that shared items read: kv, or its prefix expanded to bf16
   const int32_t* seq_ids;      // [T]; negative: a padding token
   const int32_t* idx;          // [T, top_k] positions, or nullptr: every position below key_lens
   int32_t top_k;
@@ -236,11 +239,12 @@ struct AttnArgs {
   float* lse;                  // [T, H] or nullptr
   float* part_o;               // [slots, T * H, 512] (slots > 1)
   float* part_lse;             // [slots, T * H]: base-2 log of each part's sum
+  void* workspace;             // attention_workspace() bytes
   int* err;
 };
 // keys: own_keys bounds the keys of each token's own part
-AttnPlan plan_attention(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, int sms);
-size_t attention_workspace(const AttnPlan& p, int64_t T, int32_t H);
+AttnPlan plan_attention(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, bool fp8, int sms);
+size_t attention_workspace(const AttnPlan& p, int64_t T, int32_t H, int64_t shared_keys);
 // returns the number of kernels launched through *launched
 cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, int* launched, cudaStream_t stream);
 

@@ -21,7 +21,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 // The page table's entry for position p (>= 0) of sequence seq: -1 past its columns.
 __device__ __forceinline__ int32_t page_entry(const LatentView& kv, int32_t seq, int32_t p) {
-  const int32_t slot = p / kv.page_size;
+  const int32_t slot = kv.page_shift >= 0 ? p >> kv.page_shift : p / kv.page_size;
   return slot < kv.max_pages ? __ldg(kv.pages + static_cast<int64_t>(seq) * kv.max_pages + slot) : -1;
 }
 
@@ -31,7 +31,8 @@ __device__ __forceinline__ int32_t page_row(const LatentView& kv, int32_t page, 
     record_error(err, DSA_DEVERR_PAGE, info);
     return -1;
   }
-  return page * kv.page_size + p % kv.page_size;         // fewer than 2^31 rows
+  const int32_t in_page = kv.page_shift >= 0 ? p & (kv.page_size - 1) : p % kv.page_size;
+  return page * kv.page_size + in_page;                  // fewer than 2^31 rows
 }
 
 // Sequence of token t: -1 for a padding token and (reported) for one outside the page table.
@@ -116,6 +117,16 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes, float scale
   return bf16x2(f.x * scale, f.y * scale);
 }
 
+__device__ __forceinline__ void st_shared16(uint32_t dst, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t src) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
+  return v;
+}
+
 struct __align__(8) Shared {
   uint64_t full[kStages][2];    // a half of a tile's keys is in shared memory (the second half with the rotated part)
   uint64_t listed[kStages];     // `valid` of a tile is written
@@ -129,6 +140,7 @@ struct __align__(8) Shared {
   int abort;
   int32_t key_end;
   int32_t limit[kAttnRows];     // keys at or past a row's limit are not its own
+  float inv[kAttnRows];         // 1 / the row's sum (0 for a row without keys)
   alignas(8) uint8_t valid[kStages][kLoadWarps];   // keys of a tile that exist, one bit each
 };
 
@@ -138,40 +150,13 @@ struct __align__(8) Shared {
 //   x 64; V is the same tile read with its values contiguous), 4 warps turn S into weights P.
 // The scores of tile i + 1 are computed while the weights of tile i are made.  Tiles go in and out in halves
 // of 256 values, so that the loads of one half run under the products of the other.
+// The roles' loops are kept small: together they have to fit the instruction cache.
 template <bool FP8>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, AttnPlan p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t smem = smem_addr(smem_raw);             // a constant, and the operands' addresses with it
-  if (warp == kFirstWarp) {
-    if (lane == 0) {
-      for (int i = 0; i < kStages; ++i) {
-        for (int h = 0; h < 2; ++h) {
-          // each loading thread once for its stores (FP8) and once for its copies
-          mbar_init(&sh.full[i][h], kLoadWarps * 32 * (FP8 && h == 1 ? 2 : 1));
-          mbar_init(&sh.empty[i][h], 1);
-        }
-        mbar_init(&sh.listed[i], kLoadWarps);
-      }
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&sh.scores[i], 1);
-        mbar_init(&sh.taken[i], kSoftmaxWarps);
-        mbar_init(&sh.weights[i], kSoftmaxWarps);
-      }
-      mbar_init(&sh.queries, kSoftmaxWarps);
-      mbar_init(&sh.drained[0], 1);
-      mbar_init(&sh.drained[1], 1);
-      sh.abort = 0;
-      sh.key_end = 0;
-      fence_barrier_init();
-    }
-    __syncwarp();
-    tmem_alloc(&sh.tmem, kTmemCols);
-    tmem_relinquish();
-  }
-  __syncthreads();
-  grid_dependency_wait();
 
   // the item
   const int n_shared = p.shared_groups * p.shared_slots;
@@ -197,20 +182,39 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
     k1 = min(k0 + p.own_chunk, a.idx ? a.top_k : a.max_keys);
     slot += p.shared_slots;
   }
-  const int32_t* idx = a.idx ? a.idx + static_cast<int64_t>(token) * a.top_k : nullptr;
-  const int lw = warp - kLoadWarp0;                      // loads: rows 8 lw .. 8 lw + 7 of every block
-  const int sub = lane >> 3, col = lane & 7;             // a lane's 16-byte column, rows sub and sub + 4
-  if (lw >= 0 && a.kv.rope) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {                        // the queries' rotated part, wanted with the first tile's
-      const int r = lw * 8 + sub + 4 * j;
-      const int qr = row0 + (r < rows ? r : 0);
-      const int t = qr / a.H, h = qr - t * a.H;
-      cp_async16(smem + r * 128 + ((col ^ (r & 7)) << 4),
-                 static_cast<const __nv_bfloat16*>(a.q_rope) + t * a.qr_t + h * a.qr_h + col * 8, r < rows);
+  const LatentView& kv = token < 0 ? a.shared : a.kv;
+  const bool fp8 = FP8 && (token >= 0 || !p.expand);
+  const bool rotated = a.kv.rope != nullptr;
+
+  if (warp == kFirstWarp) {
+    if (lane == 0) {
+      for (int i = 0; i < kStages; ++i) {
+        for (int h = 0; h < 2; ++h) {
+          mbar_init(&sh.full[i][h], fp8 ? kLoadWarps : kLoadWarps * 32);   // a warp's stores, or each thread's copies
+          mbar_init(&sh.empty[i][h], 1);
+        }
+        mbar_init(&sh.listed[i], kLoadWarps);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sh.scores[i], 1);
+        mbar_init(&sh.taken[i], kSoftmaxWarps);
+        mbar_init(&sh.weights[i], kSoftmaxWarps);
+        mbar_init(&sh.drained[i], 1);
+      }
+      mbar_init(&sh.queries, kSoftmaxWarps);
+      sh.abort = 0;
+      sh.key_end = 0;
+      fence_barrier_init();
     }
+    __syncwarp();
+    tmem_alloc(&sh.tmem, kTmemCols);
+    tmem_relinquish();
   }
-  int32_t seq = a.shared_seq;
+  __syncthreads();
+  grid_dependency_wait();
+
+  const int32_t* idx = a.idx ? a.idx + static_cast<int64_t>(token) * a.top_k : nullptr;
+  int32_t seq = p.expand ? 0 : a.shared_seq;
   if (token < 0) {
     if (tid < kAttnRows) {
       int32_t n = 0;
@@ -234,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       for (int32_t k = k0 + tid; k < k1; k += 8 * kThreads) {
         int32_t e[8];                                    // loads side by side
 #pragma unroll
-        for (int x = 0; x < 8; ++x) e[x] = k + x * kThreads < k1 ? idx[k + x * kThreads] : -1;
+        for (int x = 0; x < 8; ++x) e[x] = k + x * kThreads < k1 ? __ldg(idx + k + x * kThreads) : -1;
 #pragma unroll
         for (int x = 0; x < 8; ++x)
           if (e[x] >= 0) last = k + x * kThreads + 1;
@@ -248,117 +252,139 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
   const int tiles = key_end > k0 ? (key_end - k0 + kAttnTile - 1) / kAttnTile : 0;
   tc_fence_after();
 
-  if (lw >= 0) {
+  if (warp >= kLoadWarp0) {
     // ---------------------------------------------------------------- loads
-    // This warp's key `col` of a tile, the same in the lanes of one column: its position (-1: none) is read three
-    // tiles ahead, its page two, so that neither load is waited for.
-    auto position = [&](int i) -> int32_t {
-      const int32_t k = k0 + i * kAttnTile + lw * 8 + col;
-      return k < key_end ? (idx ? __ldg(idx + k) : k) : -1;
+    const int lw = warp - kLoadWarp0;                    // rows 8 lw .. 8 lw + 7 of every block
+    const int sub = lane >> 3, col = lane & 7;           // a lane's 16-byte column, rows sub and sub + 4
+    if (rotated && tiles > 0) {
+#pragma unroll 1
+      for (int r = lw * 8 + sub; r < lw * 8 + 8; r += 4) {   // the queries' rotated part, wanted with the first tile's
+        const int qr = row0 + (r < rows ? r : 0);
+        const int t = qr / a.H, h = qr - t * a.H;
+        cp_async16(smem + r * 128 + ((col ^ (r & 7)) << 4),
+                   static_cast<const __nv_bfloat16*>(a.q_rope) + t * a.qr_t + h * a.qr_h + col * 8, r < rows);
+      }
+    }
+    // This warp's key `col` of a tile, the same in the lanes of one column: its position (-1: none) is read two tiles
+    // ahead, its page one, so that neither load is waited for.
+    int32_t pos2 = -1, pos1 = -1, page1 = -1, row = -1;
+    auto advance = [&](int n) {
+      row = pos1 < 0 ? -1 : page_row(kv, page1, pos1, a.err, token < 0 ? row0 / a.H : token);
+      page1 = pos2 < 0 ? -1 : page_entry(kv, seq, pos2);
+      pos1 = pos2;
+      const int32_t k = k0 + n * kAttnTile + lw * 8 + col;
+      pos2 = k < key_end ? (idx ? __ldg(idx + k) : k) : -1;
     };
-    auto page_of = [&](int32_t pos) -> int32_t { return pos < 0 ? -1 : page_entry(a.kv, seq, pos); };
-    auto row_of = [&](int32_t pos, int32_t page) -> int32_t {
-      return pos < 0 ? -1 : page_row(a.kv, page, pos, a.err, token < 0 ? row0 / a.H : token);
+    int st = 0;
+    uint32_t phase = 1;                                  // the stages start free
+    auto place = [&](int h) {                            // whether half h of the stage is free, for the warp as one
+      const bool ok = mbar_wait<true>(&sh.empty[st][h], phase, &sh.abort);
+      return __all_sync(0xffffffffu, ok);
     };
-    // 16 FP8 codes of each half of four of the warp's rows: row 2 j + pair, codes from 16 vec.  Eight neighbouring lanes
-    // hold four neighbouring vectors of an even and of an odd row, whose places fall on different banks.
-    const int pair = (lane >> 2) & 1, vec = (lane & 3) + 4 * (lane >> 3);
-    uint4 codes[2][4];
-    float scale = 0.f;
-    auto fetch = [&](int32_t row) {
-      scale = row >= 0 ? __ldg(a.kv.scale + row) : 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int32_t rj = __shfl_sync(0xffffffffu, row, 2 * j + pair);
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.kv.latent) + static_cast<int64_t>(rj) * kLatentDim) + vec;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) codes[h][j] = rj >= 0 ? __ldg(src + 16 * h) : make_uint4(0u, 0u, 0u, 0u);
+    auto list = [&](uint32_t valid) {
+      if (lane == 0) {
+        sh.valid[st][lw] = static_cast<uint8_t>(valid);
+        mbar_arrive(&sh.listed[st]);
       }
     };
-    const int32_t pos0 = position(0), pos1 = position(1);
-    int32_t pos2 = position(2), pos3 = position(3);
-    const int32_t page0 = page_of(pos0), page1 = page_of(pos1);
-    int32_t page2 = page_of(pos2);
-    int32_t row = row_of(pos0, page0), next = row_of(pos1, page1);
-    if constexpr (FP8) fetch(row);
-    bool ok = true;
-    for (int i = 0; i < tiles; ++i) {
-      const int st = i % kStages;
-      const uint32_t parity = ((i / kStages) - 1) & 1;
-      const uint32_t stage = smem + kOffK + st * kStage;
-      const uint32_t valid = __ballot_sync(0xffffffffu, row >= 0) & 0xFFu;
-      uint32_t wide[2][4][8];                            // the codes' values in bf16
-      if constexpr (FP8) {
+    auto next_stage = [&] {
+      if (++st == kStages) {
+        st = 0;
+        phase ^= 1;
+      }
+    };
+    if (!fp8) {
+      for (int n = 0; n < tiles + 2; ++n) {
+        advance(n);                                      // the rows of tile n - 2
+        if (n < 2) continue;
+        const uint32_t valid = __ballot_sync(0xffffffffu, row >= 0) & 0xFFu;
+        const uint32_t stage = smem + kOffK + st * kStage + lw * 8 * 128;
+        const int32_t ra = __shfl_sync(0xffffffffu, row, sub), rb = __shfl_sync(0xffffffffu, row, sub + 4);
+        const __nv_bfloat16* sa = static_cast<const __nv_bfloat16*>(kv.latent) + static_cast<int64_t>(max(ra, 0)) * kLatentDim + col * 8;
+        const __nv_bfloat16* sb = static_cast<const __nv_bfloat16*>(kv.latent) + static_cast<int64_t>(max(rb, 0)) * kLatentDim + col * 8;
+        const uint32_t da = stage + sub * 128 + ((col ^ sub) << 4), db = stage + (sub + 4) * 128 + ((col ^ (sub + 4)) << 4);
+        bool ok = true;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float s = __shfl_sync(0xffffffffu, scale, 2 * j + pair);
+        for (int h = 0; h < 2; ++h) {
+          ok = place(h);
+          if (!ok) break;
+          if (h == 1) list(valid);
+#pragma unroll
+          for (int c = h * kHalf; c < h * kHalf + kHalf; ++c) {
+            cp_async16(da + c * kBlock, sa + c * 64, ra >= 0);
+            cp_async16(db + c * kBlock, sb + c * 64, rb >= 0);
+          }
+          if (h == 1 && rotated) {
+            const __nv_bfloat16* rope = static_cast<const __nv_bfloat16*>(kv.rope) + col * 8;
+            cp_async16(da + kRotated, rope + static_cast<int64_t>(max(ra, 0)) * kLatentRope, ra >= 0);
+            cp_async16(db + kRotated, rope + static_cast<int64_t>(max(rb, 0)) * kLatentRope, rb >= 0);
+          }
+          cp_async_arrive(&sh.full[st][h]);              // when this thread's copies so far have landed
+        }
+        if (!ok) break;
+        next_stage();
+      }
+    } else {
+      // FP8 rows come through registers, a tile ahead: 16 codes of each half of four of the warp's rows, row
+      // 2 j + pair, codes from 16 vec.  Eight neighbouring lanes hold four neighbouring vectors of an even and of an
+      // odd row, whose places fall on different banks.
+      const int pair = (lane >> 2) & 1, vec = (lane & 3) + 4 * (lane >> 3);
+      uint4 codes[2][4], turned[2];
+      float scale = 0.f;
+      uint32_t valid = 0;
+      for (int n = 0; n < tiles + 3; ++n) {
+        advance(n);                                      // the rows of tile n - 2
+        if (n >= 3) {
+          const uint32_t stage = smem + kOffK + st * kStage + lw * 8 * 128;
+          bool ok = true;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t w[4] = {codes[h][j].x, codes[h][j].y, codes[h][j].z, codes[h][j].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              wide[h][j][2 * e] = e4m3x2_to_bf16x2(w[e] & 0xFFFFu, s);
-              wide[h][j][2 * e + 1] = e4m3x2_to_bf16x2(w[e] >> 16, s);
+            ok = place(h);
+            if (!ok) break;
+            if (h == 1) {
+              list(valid);
+              if (rotated) {
+                st_shared16(stage + kRotated + sub * 128 + ((col ^ sub) << 4), turned[0]);
+                st_shared16(stage + kRotated + (sub + 4) * 128 + ((col ^ (sub + 4)) << 4), turned[1]);
+              }
             }
-          }
-        }
-      }
-      if constexpr (FP8) fetch(next);                    // before the wait for this tile's place
+            // two 16-byte columns of block vec / 4
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (i >= kStages) {
-          ok = mbar_wait<true>(&sh.empty[st][h], parity, &sh.abort);
-          ok = __all_sync(0xffffffffu, ok);              // a warp leaves as one
+            for (int j = 0; j < 4; ++j) {
+              const int r8 = 2 * j + pair;
+              const float s = __shfl_sync(0xffffffffu, scale, r8);
+              const uint32_t w[4] = {codes[h][j].x, codes[h][j].y, codes[h][j].z, codes[h][j].w};
+              const uint32_t base = stage + (h * kHalf + (vec >> 2)) * kBlock + r8 * 128;
+#pragma unroll
+              for (int x = 0; x < 2; ++x)
+                st_shared16(base + ((((vec & 3) * 2 + x) ^ r8) << 4),
+                            make_uint4(e4m3x2_to_bf16x2(w[2 * x] & 0xFFFFu, s), e4m3x2_to_bf16x2(w[2 * x] >> 16, s),
+                                       e4m3x2_to_bf16x2(w[2 * x + 1] & 0xFFFFu, s), e4m3x2_to_bf16x2(w[2 * x + 1] >> 16, s)));
+            }
+            cp_async_wait_all();                         // the queries' rotated part, with the first tile
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.full[st][h]);
+          }
           if (!ok) break;
+          next_stage();
         }
-        if (h == 1 && lane == 0) {
-          sh.valid[st][lw] = static_cast<uint8_t>(valid);
-          mbar_arrive(&sh.listed[st]);
+        valid = __ballot_sync(0xffffffffu, row >= 0) & 0xFFu;
+        scale = row >= 0 ? __ldg(kv.scale + row) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int32_t rj = __shfl_sync(0xffffffffu, row, 2 * j + pair);
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv.latent) + static_cast<int64_t>(rj) * kLatentDim) + vec;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) codes[h][j] = rj >= 0 ? __ldg(src + 16 * h) : make_uint4(0u, 0u, 0u, 0u);
         }
-        if constexpr (!FP8) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int r8 = sub + 4 * j;
-            const int32_t rj = __shfl_sync(0xffffffffu, row, r8);
-            const uint32_t dst = stage + h * kHalf * kBlock + (lw * 8 + r8) * 128 + ((col ^ r8) << 4);
-            const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.kv.latent) + static_cast<int64_t>(max(rj, 0)) * kLatentDim + h * 256 + col * 8;
-#pragma unroll
-            for (int c = 0; c < kHalf; ++c) cp_async16(dst + c * kBlock, src + c * 64, rj >= 0);
-          }
+        for (int j = 0; j < 2; ++j) {
+          const int32_t rj = __shfl_sync(0xffffffffu, row, sub + 4 * j);
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(kv.rope) + static_cast<int64_t>(rj) * kLatentRope) + col;
+          turned[j] = rotated && rj >= 0 ? __ldg(src) : make_uint4(0u, 0u, 0u, 0u);
         }
-        if (h == 1 && a.kv.rope) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int r8 = sub + 4 * j;
-            const int32_t rj = __shfl_sync(0xffffffffu, row, r8);
-            cp_async16(stage + kRotated + (lw * 8 + r8) * 128 + ((col ^ r8) << 4),
-                       static_cast<const __nv_bfloat16*>(a.kv.rope) + static_cast<int64_t>(max(rj, 0)) * kLatentRope + col * 8, rj >= 0);
-          }
-        }
-        if constexpr (FP8) {
-          // two 16-byte columns of block vec / 4
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int r8 = 2 * j + pair;
-            const uint32_t* v = wide[h][j];
-            const uint32_t base = stage + (h * kHalf + (vec >> 2)) * kBlock + (lw * 8 + r8) * 128;
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + ((((vec & 3) * 2 + x) ^ r8) << 4)), "r"(v[4 * x]),
-                           "r"(v[4 * x + 1]), "r"(v[4 * x + 2]), "r"(v[4 * x + 3])
-                           : "memory");
-          }
-          fence_proxy_async_smem();
-          mbar_arrive(&sh.full[st][h]);
-        }
-        if (!FP8 || h == 1) cp_async_arrive(&sh.full[st][h]);   // when this thread's copies so far have landed
       }
-      if (!ok) break;
-      row = next;
-      next = row_of(pos2, page2);
-      page2 = page_of(pos3);
-      pos2 = pos3;
-      pos3 = position(i + 4);
     }
     cp_async_wait_all();
   } else if (warp == kFirstWarp) {
@@ -392,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
           for (int ks = 0; ks < 4; ++ks)
             umma_f16_ts(d + kUpperLanes, kTmemQ + (c * 4 + ks) * 8 + kUpperLanes,
                         sdesc_kmajor_sw128(stage + (kHalf + c) * kBlock + ks * 32), idesc, c > 0 || ks > 0);
-        if (a.kv.rope) {
+        if (rotated) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
             umma_f16(d + kUpperLanes, sdesc_kmajor_sw128(smem + ks * 32), sdesc_kmajor_sw128(stage + kRotated + ks * 32), idesc, 1);
@@ -448,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       const int qr = row0 + (r < rows ? r : 0);
       const int t = qr / a.H, h = qr - t * a.H;
       const uint4* ql = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_latent) + t * a.ql_t + h * a.ql_h + (lane >> 4) * 256);
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < 128; c += 64) {
         uint4 x[16];
 #pragma unroll
@@ -468,9 +494,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.queries);
     }
+    int st = 0;
+    uint32_t phase = 0;
     for (int i = 0; i < tiles; ++i) {
       ok = mbar_wait<true>(&sh.scores[i & 1], (i >> 1) & 1, &sh.abort);
-      ok = ok && mbar_wait<true>(&sh.listed[i % kStages], (i / kStages) & 1, &sh.abort);
+      ok = ok && mbar_wait<true>(&sh.listed[st], phase, &sh.abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -478,30 +506,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       uint32_t raw[32], raw2[32];                        // the scores over either half of the values
       tmem_ld_16x256b_x8(tile, raw);
       tmem_ld_16x256b_x8(tile + kUpperLanes, raw2);
-      const uint64_t present = *reinterpret_cast<const uint64_t*>(sh.valid[i % kStages]);
+      const uint64_t present = *reinterpret_cast<const uint64_t*>(sh.valid[st]);
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.taken[i & 1]);
       float x[2][16];
       const int32_t kb = k0 + i * kAttnTile;
-      uint64_t mask[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int32_t n = limit[r] - kb;                 // the row's keys of this tile
-        mask[r] = n >= kAttnTile ? present : n <= 0 ? 0ull : present & ((1ull << n) - 1);
-      }
-      const bool whole = __all_sync(0xffffffffu, (mask[0] & mask[1]) == ~0ull);
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) x[r][2 * j + e] = __uint_as_float(raw[4 * j + 2 * r + e]) + __uint_as_float(raw2[4 * j + 2 * r + e]);
-      if (!whole) {
+          for (int e = 0; e < 2; ++e)
+            x[r][2 * j + e] = __uint_as_float(raw[4 * j + 2 * r + e]) + __uint_as_float(raw2[4 * j + 2 * r + e]);
+      const bool whole = present == ~0ull && limit[0] - kb >= kAttnTile && limit[1] - kb >= kAttnTile;
+      if (!__all_sync(0xffffffffu, whole)) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const uint64_t mine = mask[r] >> (2 * (lane & 3));
+          const int32_t n = limit[r] - kb;               // the row's keys of this tile
+          uint64_t mine = n >= kAttnTile ? present : n <= 0 ? 0ull : present & ((1ull << n) - 1);
+          mine >>= 2 * (lane & 3);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -529,20 +554,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
           m[r] = mn;
         }
       }
+      const uint32_t place = smem + kOffK + st * kStage + kRotated + (warp * 16 + fr) * 128 + (lane & 3) * 4;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float ref = m[r] == -INFINITY ? 0.f : m[r];
-        const uint32_t dst = smem + kOffK + (i % kStages) * kStage + kRotated + (warp * 16 + fr + 8 * r) * 128 + (lane & 3) * 4;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float lo = exp2_fast(fmaf(x[r][2 * j], a.scale_log2, -ref)), hi = exp2_fast(fmaf(x[r][2 * j + 1], a.scale_log2, -ref));
           l[r] += lo + hi;                               // the sum keeps fp32; the product's operand is bf16
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + ((j ^ fr) << 4)), "r"(bf16x2(lo, hi)) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(place + r * 1024 + ((j ^ fr) << 4)), "r"(bf16x2(lo, hi)) : "memory");
         }
       }
       if (rescale && i > 0) {
         // the output of the tiles before this one, complete, times the factor
-        ok = mbar_wait<true>(&sh.empty[(i - 1) % kStages][1], ((i - 1) / kStages) & 1, &sh.abort);
+        const int before = st == 0 ? kStages - 1 : st - 1;
+        ok = mbar_wait<true>(&sh.empty[before][1], st == 0 ? phase ^ 1 : phase, &sh.abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -565,43 +591,48 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.weights[i & 1]);
+      if (++st == kStages) {
+        st = 0;
+        phase ^= 1;
+      }
     }
-    launch_dependents();
-    // ---------------------------------------------------------------- the result
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      const int at = warp * 16 + fr + 8 * r;
+      if ((lane & 3) == 0 && ok) {
+        sh.inv[at] = l[r] == 0.f ? 0.f : 1.f / l[r];
+        const float lse2 = l[r] == 0.f ? -INFINITY : m[r] + log2f(l[r]);
+        if (at < rows) {
+          if (p.slots() > 1) a.part_lse[static_cast<int64_t>(slot) * a.T * a.H + row0 + at] = lse2;
+          else if (a.lse) a.lse[row0 + at] = lse2 * kLn2;
+        }
+      }
     }
-    // from the score layout to the output's: lane -> row lane % 16, values 256 (lane / 16) ..
-    const int src = (lane & 7) * 4;
-    const float l0 = __shfl_sync(0xffffffffu, l[0], src), l1 = __shfl_sync(0xffffffffu, l[1], src);
-    const float m0 = __shfl_sync(0xffffffffu, m[0], src), m1 = __shfl_sync(0xffffffffu, m[1], src);
-    const float sum = lane & 8 ? l1 : l0, top = lane & 8 ? m1 : m0;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const float lse2 = sum == 0.f ? -INFINITY : top + log2f(sum);
-    const int r = warp * 16 + (lane & 15);
-    const bool mine = r < rows;
-    const bool parts = p.slots() > 1;
-    const int64_t orow = (parts ? static_cast<int64_t>(slot) * a.T * a.H : 0) + row0 + r;
-    if (tiles > 0 && ok) {
-      // every product of the CTA: the stages take the result next
-      ok = mbar_wait<true>(&sh.empty[(tiles - 1) % kStages][1], ((tiles - 1) / kStages) & 1, &sh.abort);
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-    }
-    if (ok && mine && lane < 16) {
-      if (parts) a.part_lse[orow] = lse2;
-      else if (a.lse) a.lse[orow] = lse2 * kLn2;
-    }
-    if (ok && (tiles > 0 || !parts)) {
-      const uint32_t stride = parts ? kOutRow32 : kOutRow16;
+  }
+
+  // ---------------------------------------------------------------- the result
+  // Every product is done and every copy has landed; the keys' place takes the result, whose rows then go out whole.
+  launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const bool parts = p.slots() > 1;
+  const bool given_up = *const_cast<volatile int*>(&sh.abort) != 0;
+  if (given_up) {
+    if (tid == 0) record_error(a.err, DSA_DEVERR_TIMEOUT, static_cast<int>(blockIdx.x));
+  } else if (tiles > 0 || !parts) {
+    const uint32_t stride = parts ? kOutRow32 : kOutRow16;
+    if (warp < 12) {                                     // three warps for each of the tensor memory's quarters
+      const int r = (warp & 3) * 16 + (lane & 15);
+      const float inv = sh.inv[r];
       const uint32_t mem = smem + kOffK + r * stride + (lane >> 4) * (parts ? 1024 : 512);
 #pragma unroll 1
-      for (int c = 0; c < 256; c += 32) {
+      for (int c = (warp >> 2) * 32; c < 256; c += 96) {
         uint32_t o[32];
         if (tiles > 0) {
-          tmem_ld_32x32b_x32(quadrant + kTmemO + c, o);
+          tmem_ld_32x32b_x32((static_cast<uint32_t>((warp & 3) * 32) << 16) + kTmemO + c, o);
           tmem_ld_wait();
         } else {
 #pragma unroll
@@ -610,40 +641,58 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
         // a row without keys is zero whatever its weights' products with foreign keys left
         float val[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) val[e] = sum == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
+        for (int e = 0; e < 32; ++e) val[e] = inv == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
         if (parts) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
-            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mem + (c + e) * 4), "f"(val[e]), "f"(val[e + 1]),
-                         "f"(val[e + 2]), "f"(val[e + 3])
-                         : "memory");
+            st_shared16(mem + (c + e) * 4, make_uint4(__float_as_uint(val[e]), __float_as_uint(val[e + 1]),
+                                                      __float_as_uint(val[e + 2]), __float_as_uint(val[e + 3])));
         } else {
 #pragma unroll
           for (int e = 0; e < 32; e += 8)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mem + (c + e) * 2), "r"(bf16x2(val[e], val[e + 1])),
-                         "r"(bf16x2(val[e + 2], val[e + 3])), "r"(bf16x2(val[e + 4], val[e + 5])),
-                         "r"(bf16x2(val[e + 6], val[e + 7]))
-                         : "memory");
+            st_shared16(mem + (c + e) * 2, make_uint4(bf16x2(val[e], val[e + 1]), bf16x2(val[e + 2], val[e + 3]),
+                                                      bf16x2(val[e + 4], val[e + 5]), bf16x2(val[e + 6], val[e + 7])));
         }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (mine && lane < 16) {                           // a row each, whole
-        if (parts)
-          bulk_store(a.part_o + orow * kLatentDim, smem + kOffK + r * kOutRow32, kLatentDim * 4);
-        else
-          bulk_store(static_cast<__nv_bfloat16*>(a.out) + orow * kLatentDim, smem + kOffK + r * kOutRow16, kLatentDim * 2);
-      }
-      bulk_store_wait_read();
     }
+    tc_fence_before();
+    __syncthreads();
+    const int vecs = parts ? kLatentDim / 4 : kLatentDim / 8;      // 16-byte vectors of a row
+    uint4* out = parts ? reinterpret_cast<uint4*>(a.part_o) + (static_cast<int64_t>(slot) * a.T * a.H + row0) * vecs
+                       : static_cast<uint4*>(a.out) + static_cast<int64_t>(row0) * vecs;
+    for (int v = tid; v < rows * vecs; v += kThreads)
+      out[v] = ld_shared16(smem + kOffK + v / vecs * stride + (v % vecs) * 16);
   }
-  if (*const_cast<volatile int*>(&sh.abort) && lane == 0) record_error(a.err, DSA_DEVERR_TIMEOUT, static_cast<int>(blockIdx.x));
   tc_fence_before();
   __syncthreads();
   if (warp == kFirstWarp) {
     tc_fence_after();
     tmem_dealloc(sh.tmem, kTmemCols);
   }
+}
+
+// The shared prefix of an FP8 cache in bf16, one row per position, for the many groups of rows that read it: map[p] is p,
+// or -1 where the page table has no page.  One warp per position.
+__global__ void __launch_bounds__(256) expand_kernel(LatentView kv, int32_t seq, int32_t n, __nv_bfloat16* latent,
+                                                     __nv_bfloat16* rope, int32_t* map) {
+  grid_dependency_wait();
+  launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int32_t p = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (p >= n) return;
+  const int32_t row = page_row(kv, page_entry(kv, seq, p), p, nullptr, 0);
+  if (lane == 0) map[p] = row < 0 ? -1 : p;
+  if (row < 0) return;
+  const float s = __ldg(kv.scale + row);
+  const uint4 c = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv.latent) + static_cast<int64_t>(row) * kLatentDim) + lane);
+  uint4* out = reinterpret_cast<uint4*>(latent + static_cast<int64_t>(p) * kLatentDim) + 2 * lane;
+  out[0] = make_uint4(e4m3x2_to_bf16x2(c.x & 0xFFFFu, s), e4m3x2_to_bf16x2(c.x >> 16, s), e4m3x2_to_bf16x2(c.y & 0xFFFFu, s),
+                      e4m3x2_to_bf16x2(c.y >> 16, s));
+  out[1] = make_uint4(e4m3x2_to_bf16x2(c.z & 0xFFFFu, s), e4m3x2_to_bf16x2(c.z >> 16, s), e4m3x2_to_bf16x2(c.w & 0xFFFFu, s),
+                      e4m3x2_to_bf16x2(c.w >> 16, s));
+  if (kv.rope && lane < 8)
+    reinterpret_cast<uint4*>(rope + static_cast<int64_t>(p) * kLatentRope)[lane] =
+        __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(kv.rope) + static_cast<int64_t>(row) * kLatentRope) + lane);
 }
 
 // Joins the parts of one row: weights 2^(lse_i - max) over their sum.  128 threads, 4 values each.
@@ -678,7 +727,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Cuts a call into items.  One size of chunk serves the shared and the own part.  An item costs its
 // tiles and about four tiles' time beside them (set-up, queries, result); splitting a row into parts costs
 // the join and the parts' traffic.  Candidates: no split, and the smallest chunks that fill 1 .. 4 waves.
-AttnPlan plan_attention(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, int sms) {
+AttnPlan plan_attention(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, bool fp8, int sms) {
   const int64_t R = T * H, shared_tiles = ceil_div(shared_keys, kAttnTile);
   // a call with no keys at all still writes its empty rows
   const int64_t own_tiles = own_keys > 0 || shared_keys == 0 ? std::max<int64_t>(1, ceil_div(own_keys, kAttnTile)) : 0;
@@ -709,14 +758,27 @@ AttnPlan plan_attention(int64_t T, int32_t H, int64_t shared_keys, int64_t own_k
     // rounding up to whole chunks can need more items than fit: grow the chunk until they do
     while (chunk < longest && consider(chunk) > room) chunk += std::max<int64_t>(1, chunk / 16);
   }
+  // Expanding FP8 rows to bf16 costs the loading warps more time than a tile's products take; a prefix that many
+  // groups of rows read is expanded once instead (23 x 128 heads over 16001 keys: EXPAND_FIGURES).
+  best.expand = fp8 && shared_groups >= 4 && shared_groups * shared_tiles >= 8 * sms;
   return best;
 }
 
-size_t attention_workspace(const AttnPlan& p, int64_t T, int32_t H) {
-  return p.slots() > 1 ? size_t(p.slots()) * T * H * (kLatentDim + 1) * sizeof(float) : 0;
+namespace {
+
+size_t part_bytes(const AttnPlan& p, int64_t T, int32_t H) {
+  const size_t b = p.slots() > 1 ? size_t(p.slots()) * T * H * (kLatentDim + 1) * sizeof(float) : 0;
+  return (b + 255) / 256 * 256;
 }
 
-cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, int* launched, cudaStream_t stream) {
+}  // namespace
+
+size_t attention_workspace(const AttnPlan& p, int64_t T, int32_t H, int64_t shared_keys) {
+  return part_bytes(p, T, H) + (p.expand ? size_t(shared_keys) * (2 * (kLatentDim + kLatentRope) + 4) : 0);
+}
+
+cudaError_t launch_attention(const AttnArgs& args, const AttnPlan& p, int* launched, cudaStream_t stream) {
+  AttnArgs a = args;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -724,6 +786,21 @@ cudaError_t launch_attention(const AttnArgs& a, const AttnPlan& p, int* launched
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  a.shared = a.kv;
+  if (p.expand) {
+    __nv_bfloat16* latent = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(a.workspace) + part_bytes(p, a.T, a.H));
+    __nv_bfloat16* rope = latent + int64_t(a.shared_len) * kLatentDim;
+    int32_t* map = reinterpret_cast<int32_t*>(rope + int64_t(a.shared_len) * kLatentRope);
+    cfg.gridDim = dim3(static_cast<unsigned>((a.shared_len + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, expand_kernel, a.kv, a.shared_seq, a.shared_len, latent, rope, map);
+    if (e != cudaSuccess) return e;
+    ++*launched;
+    // a cache of one-row pages whose only sequence is the prefix
+    a.shared = LatentView{latent, nullptr, a.kv.rope ? rope : nullptr, a.shared_len, 1, 0, 0, map, 1, a.shared_len};
+  }
+  a.part_o = static_cast<float*>(a.workspace);
+  a.part_lse = a.part_o ? a.part_o + size_t(p.slots()) * a.T * a.H * kLatentDim : nullptr;
   cfg.gridDim = dim3(static_cast<unsigned>(int64_t(p.shared_groups) * p.shared_slots + int64_t(a.T) * p.own_groups * p.own_slots));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
