@@ -462,11 +462,11 @@ def dsa_rmsnorm_fp8(x, weight, eps=1e-6, residual=None, group=128, residual_out=
         elif residual_out.dtype is not x.dtype or residual_out.numel() != n:
             raise ValueError(f"residual_out must hold {n} values of {x.dtype}")
     if codes is None:
-        codes = torch.empty((rows, d), dtype=torch.uint8, device=x.device)
+        codes = x.new_empty((rows, d), dtype=torch.uint8)
     elif codes.element_size() != 1 or codes.numel() != n:
         raise ValueError(f"codes must hold {n} bytes")
     if scale is None:
-        scale = torch.empty((rows, groups), dtype=torch.float32, device=x.device)
+        scale = x.new_empty((rows, groups), dtype=torch.float32)
     elif scale.dtype is not torch.float32 or scale.numel() != rows * groups:
         raise ValueError(f"scale must hold {rows * groups} fp32 values")
     if normed is not None and (normed.dtype is not torch.bfloat16 or normed.numel() != n):
@@ -543,17 +543,16 @@ def _latent_query(q_latent, q_rope, cache) -> _lib.LatentQuery:
 def _outputs(T, H, q_latent, out, lse, workspace, need):
     """(out, lse, workspace of `need` bytes); what is not given comes from torch's allocator, so that a captured
     graph keeps its own."""
-    dev = q_latent.device
     if out is None:
-        out = torch.empty((T, H, 512), dtype=torch.bfloat16, device=dev)
+        out = q_latent.new_empty((T, H, 512))
     elif out.dtype is not torch.bfloat16 or out.numel() != T * H * 512:
         raise ValueError("out must hold [T, H, 512] bf16 values")
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+        lse = q_latent.new_empty((T, H), dtype=torch.float32)
     elif lse.dtype is not torch.float32 or lse.numel() != T * H:
         raise ValueError("lse must hold [T, H] fp32 values")
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = q_latent.new_empty(need, dtype=torch.uint8)
     return out, lse, workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 

@@ -629,27 +629,22 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       const float inv = sh.inv[r];
       const uint32_t mem = smem + kOffK + r * stride + (lane >> 4) * (parts ? 1024 : 512);
 #pragma unroll 1
-      for (int c = (warp >> 2) * 32; c < 256; c += 96) {
-        uint32_t o[32];
-        if (tiles > 0) {
-          tmem_ld_32x32b_x32((static_cast<uint32_t>((warp & 3) * 32) << 16) + kTmemO + c, o);
-          tmem_ld_wait();
-        } else {
+      for (int c = (warp >> 2) * 16; c < 256; c += 48) {
+        uint32_t o[16];
+        tmem_ld_32x32b_x16((static_cast<uint32_t>((warp & 3) * 32) << 16) + kTmemO + c, o);
+        tmem_ld_wait();
+        // a row without keys is zero whatever its weights' products with foreign keys (or nothing at all) left
+        float val[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
-        }
-        // a row without keys is zero whatever its weights' products with foreign keys left
-        float val[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) val[e] = inv == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
+        for (int e = 0; e < 16; ++e) val[e] = inv == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
         if (parts) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
+          for (int e = 0; e < 16; e += 4)
             st_shared16(mem + (c + e) * 4, make_uint4(__float_as_uint(val[e]), __float_as_uint(val[e + 1]),
                                                       __float_as_uint(val[e + 2]), __float_as_uint(val[e + 3])));
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
+          for (int e = 0; e < 16; e += 8)
             st_shared16(mem + (c + e) * 2, make_uint4(bf16x2(val[e], val[e + 1]), bf16x2(val[e + 2], val[e + 3]),
                                                       bf16x2(val[e + 4], val[e + 5]), bf16x2(val[e + 6], val[e + 7])));
         }
@@ -657,11 +652,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
     }
     tc_fence_before();
     __syncthreads();
-    const int vecs = parts ? kLatentDim / 4 : kLatentDim / 8;      // 16-byte vectors of a row
-    uint4* out = parts ? reinterpret_cast<uint4*>(a.part_o) + (static_cast<int64_t>(slot) * a.T * a.H + row0) * vecs
-                       : static_cast<uint4*>(a.out) + static_cast<int64_t>(row0) * vecs;
-    for (int v = tid; v < rows * vecs; v += kThreads)
-      out[v] = ld_shared16(smem + kOffK + v / vecs * stride + (v % vecs) * 16);
+    const int shift = parts ? 7 : 6;                     // 16-byte vectors of a row: 512 fp32 or bf16 values
+    uint4* out = parts ? reinterpret_cast<uint4*>(a.part_o) + ((static_cast<int64_t>(slot) * a.T * a.H + row0) << shift)
+                       : static_cast<uint4*>(a.out) + (static_cast<int64_t>(row0) << shift);
+#pragma unroll 2
+    for (int v = tid; v < rows << shift; v += kThreads)
+      out[v] = ld_shared16(smem + kOffK + (v >> shift) * stride + (v & ((1 << shift) - 1)) * 16);
   }
   tc_fence_before();
   __syncthreads();
