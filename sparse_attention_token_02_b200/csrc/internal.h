@@ -217,7 +217,9 @@ constexpr int kAttnTile = 64;          // keys per tile; chunks are whole tiles
 struct AttnPlan {
   int32_t shared_groups, shared_slots, shared_chunk;
   int32_t own_groups, own_slots, own_chunk;       // own_groups: row groups of one token
+  int32_t cluster;                                // > 1: the own_slots CTAs of a row group are a cluster and join their parts there
   int32_t expand;                                 // the shared prefix of an FP8 cache goes to bf16 first
+  __host__ __device__ bool parts() const { return cluster == 1 && slots() > 1; }   // parts go to memory
   __host__ __device__ int32_t slots() const { return shared_slots + own_slots; }
 };
 struct AttnArgs {

@@ -86,6 +86,8 @@ constexpr uint32_t kTmemS = 256;
 constexpr uint32_t kTmemQ = 384;
 constexpr uint32_t kUpperLanes = 16u << 16;
 
+constexpr int kMaxCluster = 16;                              // parts of a row that a cluster joins
+
 constexpr int kSoftmaxWarps = 4;
 constexpr int kFirstWarp = 4, kSecondWarp = 5;                // issue the first and the second products
 constexpr int kLoadWarp0 = 6;
@@ -121,6 +123,16 @@ __device__ __forceinline__ void st_shared16(uint32_t dst, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+__device__ __forceinline__ void st_shared_f32(uint32_t dst, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(dst), "f"(v) : "memory");
+}
+
+__device__ __forceinline__ float ld_shared_f32(uint32_t src) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(src) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ uint4 ld_shared16(uint32_t src) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(src) : "memory");
@@ -141,6 +153,7 @@ struct __align__(8) Shared {
   int32_t key_end;
   int32_t limit[kAttnRows];     // keys at or past a row's limit are not its own
   float inv[kAttnRows];         // 1 / the row's sum (0 for a row without keys)
+  float lse2[kAttnRows];        // the base-2 log of the row's sum
   alignas(8) uint8_t valid[kStages][kLoadWarps];   // keys of a tile that exist, one bit each
 };
 
@@ -163,13 +176,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
   int item = blockIdx.x;
   int row0;                      // first of the item's rows in the packed [T, H]
   int rows, slot, token = -1;
-  int32_t k0, k1;
-  if (item < n_shared) {
+  if (p.cluster > 1) {
+    slot = item % p.cluster;
+    item /= p.cluster;
+    const int g = item % p.own_groups;
+    token = item / p.own_groups;
+    row0 = token * a.H + g * kAttnRows;
+    rows = min(kAttnRows, a.H - g * kAttnRows);
+  } else if (item < n_shared) {
     row0 = item % p.shared_groups * kAttnRows;
     rows = min(kAttnRows, a.T * a.H - row0);
     slot = item / p.shared_groups;
-    k0 = slot * p.shared_chunk;
-    k1 = min(k0 + p.shared_chunk, a.shared_len);
   } else {
     item -= n_shared;
     const int g = item % p.own_groups;
@@ -177,10 +194,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
     token = item % a.T;
     row0 = token * a.H + g * kAttnRows;
     rows = min(kAttnRows, a.H - g * kAttnRows);
-    slot = item / a.T;
-    k0 = (a.idx ? 0 : a.shared_len) + slot * p.own_chunk;
+    slot = p.shared_slots + item / a.T;
+  }
+  int32_t k0, k1;                // its keys, before lengths are known
+  if (token < 0) {
+    k0 = slot * p.shared_chunk;
+    k1 = min(k0 + p.shared_chunk, a.shared_len);
+  } else {
+    k0 = (p.shared_slots ? a.shared_len : 0) + (slot - p.shared_slots) * p.own_chunk;
     k1 = min(k0 + p.own_chunk, a.idx ? a.top_k : a.max_keys);
-    slot += p.shared_slots;
   }
   const LatentView& kv = token < 0 ? a.shared : a.kv;
   const bool fp8 = FP8 && (token >= 0 || !p.expand);
@@ -214,7 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
   grid_dependency_wait();
 
   const int32_t* idx = a.idx ? a.idx + static_cast<int64_t>(token) * a.top_k : nullptr;
-  int32_t seq = p.expand ? 0 : a.shared_seq;
+  const int32_t shared_seq = p.expand ? 0 : a.shared_seq;
+  int32_t seq = shared_seq;
   if (token < 0) {
     if (tid < kAttnRows) {
       int32_t n = 0;
@@ -270,7 +293,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
     int32_t pos2 = -1, pos1 = -1, page1 = -1, row = -1;
     auto advance = [&](int n) {
       row = pos1 < 0 ? -1 : page_row(kv, page1, pos1, a.err, token < 0 ? row0 / a.H : token);
-      page1 = pos2 < 0 ? -1 : page_entry(kv, seq, pos2);
+      // shared positions are read through the one sequence whichever item reads them
+      page1 = pos2 < 0 ? -1 : page_entry(kv, pos2 < a.shared_len ? shared_seq : seq, pos2);
       pos1 = pos2;
       const int32_t k = k0 + n * kAttnTile + lw * 8 + col;
       pos2 = k < key_end ? (idx ? __ldg(idx + k) : k) : -1;
@@ -604,8 +628,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       if ((lane & 3) == 0 && ok) {
         sh.inv[at] = l[r] == 0.f ? 0.f : 1.f / l[r];
         const float lse2 = l[r] == 0.f ? -INFINITY : m[r] + log2f(l[r]);
-        if (at < rows) {
-          if (p.slots() > 1) a.part_lse[static_cast<int64_t>(slot) * a.T * a.H + row0 + at] = lse2;
+        sh.lse2[at] = lse2;
+        if (at < rows && p.cluster == 1) {
+          if (p.parts()) a.part_lse[static_cast<int64_t>(slot) * a.T * a.H + row0 + at] = lse2;
           else if (a.lse) a.lse[row0 + at] = lse2 * kLn2;
         }
       }
@@ -618,16 +643,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const bool parts = p.slots() > 1;
+  const bool wide = p.cluster > 1 || p.parts();          // parts are fp32
   const bool given_up = *const_cast<volatile int*>(&sh.abort) != 0;
   if (given_up) {
     if (tid == 0) record_error(a.err, DSA_DEVERR_TIMEOUT, static_cast<int>(blockIdx.x));
-  } else if (tiles > 0 || !parts) {
-    const uint32_t stride = parts ? kOutRow32 : kOutRow16;
+  } else if (tiles > 0 || !wide) {
+    const uint32_t stride = wide ? kOutRow32 : kOutRow16;
     if (warp < 12) {                                     // three warps for each of the tensor memory's quarters
       const int r = (warp & 3) * 16 + (lane & 15);
       const float inv = sh.inv[r];
-      const uint32_t mem = smem + kOffK + r * stride + (lane >> 4) * (parts ? 1024 : 512);
+      const uint32_t mem = smem + kOffK + r * stride + (lane >> 4) * (wide ? 1024 : 512);
 #pragma unroll 1
       for (int c = (warp >> 2) * 16; c < 256; c += 48) {
         uint32_t o[16];
@@ -637,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
         float val[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) val[e] = inv == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
-        if (parts) {
+        if (wide) {
 #pragma unroll
           for (int e = 0; e < 16; e += 4)
             st_shared16(mem + (c + e) * 4, make_uint4(__float_as_uint(val[e]), __float_as_uint(val[e + 1]),
@@ -652,12 +677,61 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
     }
     tc_fence_before();
     __syncthreads();
-    const int shift = parts ? 7 : 6;                     // 16-byte vectors of a row: 512 fp32 or bf16 values
-    uint4* out = parts ? reinterpret_cast<uint4*>(a.part_o) + ((static_cast<int64_t>(slot) * a.T * a.H + row0) << shift)
-                       : static_cast<uint4*>(a.out) + (static_cast<int64_t>(row0) << shift);
+    if (p.cluster == 1) {
+      const int shift = wide ? 7 : 6;                    // 16-byte vectors of a row: 512 fp32 or bf16 values
+      uint4* out = wide ? reinterpret_cast<uint4*>(a.part_o) + ((static_cast<int64_t>(slot) * a.T * a.H + row0) << shift)
+                        : static_cast<uint4*>(a.out) + (static_cast<int64_t>(row0) << shift);
 #pragma unroll 2
-    for (int v = tid; v < rows << shift; v += kThreads)
-      out[v] = ld_shared16(smem + kOffK + (v >> shift) * stride + (v & ((1 << shift) - 1)) * 16);
+      for (int v = tid; v < rows << shift; v += kThreads)
+        out[v] = ld_shared16(smem + kOffK + (v >> shift) * stride + (v & ((1 << shift) - 1)) * 16);
+    }
+  }
+  if (p.cluster > 1) {
+    // The cluster's CTAs hold the parts of the same rows: each joins a share of the rows, four values a thread, from
+    // everyone's shared memory, with weights 2^(lse_i - max) over their sum.
+    cluster_arrive();
+    cluster_wait();
+    const int r0 = rows * slot / p.cluster, r1 = rows * (slot + 1) / p.cluster;
+    const uint32_t table = smem;                         // [r1 - r0][16] weights, where the queries' rotated part was
+    if (tid < r1 - r0) {
+      const uint32_t at = smem_addr(&sh.lse2[r0 + tid]);
+      float w[kMaxCluster], top = -INFINITY, total = 0.f;
+#pragma unroll
+      for (int i = 0; i < kMaxCluster; ++i) w[i] = i < p.cluster ? ld_cluster_f32(cluster_addr(at, i)) : -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kMaxCluster; ++i) top = fmaxf(top, w[i]);
+      const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int i = 0; i < kMaxCluster; ++i) total += w[i] = exp2f(w[i] - ref);
+      const float inv = total == 0.f ? 0.f : 1.f / total;
+#pragma unroll
+      for (int i = 0; i < kMaxCluster; ++i) st_shared_f32(table + (tid * kMaxCluster + i) * 4, w[i] * inv);
+      if (a.lse) a.lse[row0 + r0 + tid] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
+    }
+    __syncthreads();
+    for (int v = tid; v < (r1 - r0) * 128; v += kThreads) {
+      const int r = v >> 7, c = v & 127;
+      const uint32_t val = smem + kOffK + (r0 + r) * kOutRow32 + c * 16;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int i = 0; i < p.cluster; i += 8) {           // eight loads under way: a neighbour's memory is far
+        float4 x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (i + e < p.cluster) x[e] = ld_cluster_f32x4(cluster_addr(val, i + e));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float w = i + e < p.cluster ? ld_shared_f32(table + (r * kMaxCluster + i + e) * 4) : 0.f;
+          if (w != 0.f) {                                // else there may be nothing, or anything, in its place
+            o.x += w * x[e].x; o.y += w * x[e].y; o.z += w * x[e].z; o.w += w * x[e].w;
+          }
+        }
+      }
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + static_cast<int64_t>(row0 + r0 + r) * kLatentDim + c * 4) =
+          make_uint2(bf16x2(o.x, o.y), bf16x2(o.z, o.w));
+    }
+    cluster_arrive();                                    // nobody leaves while its shared memory is read
+    cluster_wait();
   }
   tc_fence_before();
   __syncthreads();
@@ -720,50 +794,104 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-// Cuts a call into items.  One size of chunk serves the shared and the own part.  An item costs its
-// tiles and about four tiles' time beside them (set-up, queries, result); splitting a row into parts costs
-// the join and the parts' traffic.  Candidates: no split, and the smallest chunks that fill 1 .. 4 waves.
+// Sets a kernel up for a launch on the current device, once for each device: the attributes stay with its context.
+cudaError_t set_up(bool fp8) {
+  static std::atomic<uint64_t> ready[2];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (e != cudaSuccess || (ready[fp8].load(std::memory_order_relaxed) & bit)) return e;
+  auto kernel = fp8 ? attention_kernel<true> : attention_kernel<false>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) ready[fp8].fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+// CTAs that run at once in clusters of a size (2, 4, 8, 16): a cluster's SMs belong to one GPC, so that is fewer than
+// there are SMs.  Without a device (a workspace query on a host that has none): an estimate.
+int cluster_room(int cluster, int sms) {
+  static std::atomic<int> known[64][5];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return sms / 18 * 16;
+  const int i = __builtin_ctz(cluster);
+  int room = known[dev][i].load(std::memory_order_relaxed);
+  if (room == 0) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (set_up(false) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, attention_kernel<false>, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      return sms / 18 * 16;
+    }
+    room = n * cluster;
+    known[dev][i].store(room, std::memory_order_relaxed);
+  }
+  return room;
+}
+
+// Cuts a call into items, in units of a tile's time.  An item costs its tiles and about four tiles' time beside them
+// (set-up, queries, result).  Splitting a row costs its join: in a cluster (two to sixteen parts) about two more, through
+// memory with a second kernel about five and the parts' traffic.  A token's rows are whole groups where H is a
+// multiple of 64; sharing a prefix then saves no tile, and shared positions are read by the tokens' own items.
 AttnPlan plan_attention(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, bool fp8, int sms) {
-  const int64_t R = T * H, shared_tiles = ceil_div(shared_keys, kAttnTile);
+  const int64_t R = T * H, shared_groups = ceil_div(R, kAttnRows), own_groups = ceil_div(H, kAttnRows);
+  int64_t shared_tiles = ceil_div(shared_keys, kAttnTile);
+  // Expanding FP8 rows to bf16 costs the loading warps more time than a tile's products take; a prefix that many
+  // groups of rows read is expanded once instead (23 x 128 heads over 16001 keys: 248 -> 173 us).
+  const bool expand = fp8 && shared_groups >= 4 && shared_groups * shared_tiles >= 8 * sms;
+  if (H % kAttnRows == 0 && !expand) {
+    own_keys += shared_keys;
+    shared_tiles = 0;
+  }
   // a call with no keys at all still writes its empty rows
-  const int64_t own_tiles = own_keys > 0 || shared_keys == 0 ? std::max<int64_t>(1, ceil_div(own_keys, kAttnTile)) : 0;
+  const int64_t own_tiles = own_keys > 0 || shared_tiles == 0 ? std::max<int64_t>(1, ceil_div(own_keys, kAttnTile)) : 0;
   const int64_t longest = std::max(shared_tiles, own_tiles);
-  const int64_t shared_groups = ceil_div(R, kAttnRows), own_groups = ceil_div(H, kAttnRows);
   AttnPlan best{};
   double best_cost = 0.0;
-  auto consider = [&](int64_t chunk) {
+  auto consider = [&](int64_t chunk, int cluster) {
     AttnPlan p{};
     p.shared_groups = static_cast<int32_t>(shared_groups);
     p.own_groups = static_cast<int32_t>(own_groups);
     p.shared_slots = static_cast<int32_t>(ceil_div(shared_tiles, chunk));
-    p.own_slots = static_cast<int32_t>(ceil_div(own_tiles, chunk));
+    p.own_slots = cluster > 1 ? cluster : static_cast<int32_t>(ceil_div(own_tiles, chunk));
     p.shared_chunk = p.own_chunk = static_cast<int32_t>(chunk * kAttnTile);
+    p.cluster = cluster;
+    p.expand = expand;
     const int64_t items = shared_groups * p.shared_slots + T * own_groups * p.own_slots;
-    const double cost = ceil_div(items, sms) * (chunk + 4.0) + (p.slots() > 1 ? 3.0 + double(p.slots()) * R * 0.0006 : 0.0);
+    const double join = cluster > 1 ? 2.0 : p.slots() > 1 ? 5.0 + double(p.slots()) * R * 0.0006 : 0.0;
+    const double cost = ceil_div(items, cluster > 1 ? cluster_room(cluster, sms) : sms) * (chunk + 4.0) + join;
     if (best.slots() == 0 || cost < best_cost) {
       best = p;
       best_cost = cost;
     }
     return items;
   };
-  consider(longest);
+  consider(longest, 1);
+  if (shared_tiles == 0)
+    for (int cluster = 2; cluster <= kMaxCluster && cluster <= own_tiles; cluster *= 2) consider(ceil_div(own_tiles, cluster), cluster);
   const int64_t tiles = shared_groups * shared_tiles + T * own_groups * own_tiles;
   for (int waves = 1; waves <= 4; ++waves) {
     const int64_t room = int64_t(waves) * sms;
     int64_t chunk = std::min(longest, ceil_div(tiles, room));
     // rounding up to whole chunks can need more items than fit: grow the chunk until they do
-    while (chunk < longest && consider(chunk) > room) chunk += std::max<int64_t>(1, chunk / 16);
+    while (chunk < longest && consider(chunk, 1) > room) chunk += std::max<int64_t>(1, chunk / 16);
   }
-  // Expanding FP8 rows to bf16 costs the loading warps more time than a tile's products take; a prefix that many
-  // groups of rows read is expanded once instead (23 x 128 heads over 16001 keys: EXPAND_FIGURES).
-  best.expand = fp8 && shared_groups >= 4 && shared_groups * shared_tiles >= 8 * sms;
   return best;
 }
 
 namespace {
 
 size_t part_bytes(const AttnPlan& p, int64_t T, int32_t H) {
-  const size_t b = p.slots() > 1 ? size_t(p.slots()) * T * H * (kLatentDim + 1) * sizeof(float) : 0;
+  const size_t b = p.parts() ? size_t(p.slots()) * T * H * (kLatentDim + 1) * sizeof(float) : 0;
   return (b + 255) / 256 * 256;
 }
 
@@ -775,7 +903,7 @@ size_t attention_workspace(const AttnPlan& p, int64_t T, int32_t H, int64_t shar
 
 cudaError_t launch_attention(const AttnArgs& args, const AttnPlan& p, int* launched, cudaStream_t stream) {
   AttnArgs a = args;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
@@ -801,21 +929,18 @@ cudaError_t launch_attention(const AttnArgs& args, const AttnPlan& p, int* launc
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   auto kernel = a.kv.fp8 ? attention_kernel<true> : attention_kernel<false>;
-  // once per device and kernel: the attribute stays with the device's context
-  static std::atomic<uint64_t> ready[2];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = set_up(a.kv.fp8);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if (!(ready[a.kv.fp8].load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return e;
-    ready[a.kv.fp8].fetch_or(bit, std::memory_order_relaxed);
+  if (p.cluster > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
   }
   e = cudaLaunchKernelEx(&cfg, kernel, a, p);
   if (e != cudaSuccess) return e;
   ++*launched;
-  if (p.slots() > 1) {
+  if (p.parts()) {
     cfg.gridDim = dim3(static_cast<unsigned>(int64_t(a.T) * a.H));
     cfg.blockDim = dim3(128);
     cfg.dynamicSmemBytes = 0;
