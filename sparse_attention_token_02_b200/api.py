@@ -279,8 +279,7 @@ def _run_compressed(fn_name, q, cache, w, seq_lens, q_lens, m, top_k, q_scale, k
 
 
 def _rope(d, rope_dim, base, interleaved):
-    from ._lib import Rope
-    return Rope(d if rope_dim is None else int(rope_dim), 1 if interleaved else 0, float(base))
+    return _lib.Rope(d if rope_dim is None else int(rope_dim), 1 if interleaved else 0, float(base))
 
 
 def dsa_indexer_kcache_append_rope(cache: IndexerKCache, k_new, dst_rows, positions, rope_dim=None, base=10000.0,

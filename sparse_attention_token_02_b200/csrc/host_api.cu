@@ -833,14 +833,19 @@ dsa_status_t run_indexer(Mode mode, const dsa_query_t* q, const dsa_kcache_t* kc
 
 }  // namespace
 
-// RoPE parameters for the kernels, with the pair frequencies base^(-2i / rope_dim) in fp64
+// RoPE parameters for the kernels, with the pair frequencies base^(-2i / rope_dim) in fp64.  They depend on the
+// three numbers alone, and 64 powers take as long as a launch: the last ones of the thread are kept.
 RopeParams rope_params(const dsa_rope_t& r) {
-  RopeParams p{};
+  thread_local RopeParams p{};
+  thread_local bool known = false;
+  if (known && p.rope_dim == r.rope_dim && p.interleaved == r.interleaved && p.base == r.base) return p;
+  p = RopeParams{};
   p.rope_dim = r.rope_dim;
   p.interleaved = r.interleaved;
   p.base = r.base;
   for (int i = 0; i < kRopeMaxPairs; ++i)
     p.inv_freq[i] = (r.rope_dim > 0 && r.base > 0.0) ? std::pow(r.base, -2.0 * i / r.rope_dim) : 0.0;
+  known = true;
   return p;
 }
 

@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
   }
   const LatentView& kv = token < 0 ? a.shared : a.kv;
   const bool fp8 = FP8 && (token >= 0 || !p.expand);
+  const int stages = fp8 ? kStages - 1 : kStages;
   const bool rotated = a.kv.rope != nullptr;
 
   if (warp == kFirstWarp) {
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       }
     };
     auto next_stage = [&] {
-      if (++st == kStages) {
+      if (++st == stages) {
         st = 0;
         phase ^= 1;
       }
@@ -349,35 +350,42 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
         next_stage();
       }
     } else {
-      // FP8 rows come through registers, a tile ahead: 16 codes of each half of four of the warp's rows, row
-      // 2 j + pair, codes from 16 vec.  Eight neighbouring lanes hold four neighbouring vectors of an even and of an
-      // odd row, whose places fall on different banks.
+      // FP8 rows come through the place of the third stage, two tiles ahead: every warp copies its own eight rows there
+      // (512 bytes each) and expands them from there.  The 16 codes vec of row 2 j + pair are a lane's: eight
+      // neighbouring lanes hold four vectors of an even and of an odd row, whose places in an operand block fall on
+      // different banks, and so do theirs in the codes' (an odd row's vectors sit four places on).
       const int pair = (lane >> 2) & 1, vec = (lane & 3) + 4 * (lane >> 3);
-      uint4 codes[2][4], turned[2];
-      float scale = 0.f;
-      uint32_t valid = 0;
-      for (int n = 0; n < tiles + 3; ++n) {
+      const uint32_t ring = smem + kOffK + (kStages - 1) * kStage + lw * 4096;
+      // scales, existing keys and rotated parts of the tiles n - 3 and n - 4 (their rows sub and sub + 4, column col)
+      float scale1 = 0.f, scale2 = 0.f;
+      uint32_t valid1 = 0, valid2 = 0;
+      uint4 turned1[2], turned2[2];
+      for (int n = 0; n < tiles + 4; ++n) {
         advance(n);                                      // the rows of tile n - 2
-        if (n >= 3) {
+        const uint32_t codes = ring + (n & 1) * 32768;
+        if (n >= 4) {
           const uint32_t stage = smem + kOffK + st * kStage + lw * 8 * 128;
+          cp_async_wait<1>();                            // all but the latest tile's codes
+          __syncwarp();
           bool ok = true;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             ok = place(h);
             if (!ok) break;
             if (h == 1) {
-              list(valid);
+              list(valid2);
               if (rotated) {
-                st_shared16(stage + kRotated + sub * 128 + ((col ^ sub) << 4), turned[0]);
-                st_shared16(stage + kRotated + (sub + 4) * 128 + ((col ^ (sub + 4)) << 4), turned[1]);
+                st_shared16(stage + kRotated + sub * 128 + ((col ^ sub) << 4), turned2[0]);
+                st_shared16(stage + kRotated + (sub + 4) * 128 + ((col ^ (sub + 4)) << 4), turned2[1]);
               }
             }
             // two 16-byte columns of block vec / 4
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int r8 = 2 * j + pair;
-              const float s = __shfl_sync(0xffffffffu, scale, r8);
-              const uint32_t w[4] = {codes[h][j].x, codes[h][j].y, codes[h][j].z, codes[h][j].w};
+              const float s = __shfl_sync(0xffffffffu, scale2, r8);
+              const uint4 u = ld_shared16(codes + r8 * 512 + (((h * 16 + vec) ^ (pair << 2)) << 4));
+              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
               const uint32_t base = stage + (h * kHalf + (vec >> 2)) * kBlock + r8 * 128;
 #pragma unroll
               for (int x = 0; x < 2; ++x)
@@ -385,7 +393,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
                             make_uint4(e4m3x2_to_bf16x2(w[2 * x] & 0xFFFFu, s), e4m3x2_to_bf16x2(w[2 * x] >> 16, s),
                                        e4m3x2_to_bf16x2(w[2 * x + 1] & 0xFFFFu, s), e4m3x2_to_bf16x2(w[2 * x + 1] >> 16, s)));
             }
-            cp_async_wait_all();                         // the queries' rotated part, with the first tile
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.full[st][h]);
@@ -393,21 +400,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
           if (!ok) break;
           next_stage();
         }
-        valid = __ballot_sync(0xffffffffu, row >= 0) & 0xFFu;
-        scale = row >= 0 ? __ldg(kv.scale + row) : 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int32_t rj = __shfl_sync(0xffffffffu, row, 2 * j + pair);
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv.latent) + static_cast<int64_t>(rj) * kLatentDim) + vec;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) codes[h][j] = rj >= 0 ? __ldg(src + 16 * h) : make_uint4(0u, 0u, 0u, 0u);
-        }
+        scale2 = scale1;
+        valid2 = valid1;
+        scale1 = row >= 0 ? __ldg(kv.scale + row) : 0.f;
+        valid1 = __ballot_sync(0xffffffffu, row >= 0) & 0xFFu;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int32_t rj = __shfl_sync(0xffffffffu, row, sub + 4 * j);
           const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(kv.rope) + static_cast<int64_t>(rj) * kLatentRope) + col;
-          turned[j] = rotated && rj >= 0 ? __ldg(src) : make_uint4(0u, 0u, 0u, 0u);
+          turned2[j] = turned1[j];
+          turned1[j] = rotated && rj >= 0 ? __ldg(src) : make_uint4(0u, 0u, 0u, 0u);
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int32_t rj = __shfl_sync(0xffffffffu, row, j);
+          cp_async16(codes + j * 512 + ((lane ^ ((j & 1) << 2)) << 4),
+                     static_cast<const uint8_t*>(kv.latent) + static_cast<int64_t>(max(rj, 0)) * kLatentDim + lane * 16, rj >= 0);
+        }
+        cp_async_commit();
       }
     }
     cp_async_wait_all();
@@ -448,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
             umma_f16(d + kUpperLanes, sdesc_kmajor_sw128(smem + ks * 32), sdesc_kmajor_sw128(stage + kRotated + ks * 32), idesc, 1);
         }
         umma_commit(&sh.scores[i & 1]);
-        if (++st == kStages) {
+        if (++st == stages) {
           st = 0;
           phase ^= 1;
         }
@@ -477,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
                      sdesc_mnmajor_sw128(stage + h * kHalf * kBlock + ks * 2048, kBlock), idesc, i > 0 || ks > 0);
           umma_commit(&sh.empty[st][h]);
         }
-        if (++st == kStages) st = 0;
+        if (++st == stages) st = 0;
       }
       umma_commit(&sh.drained[1]);
       int alone = 0;
@@ -591,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       }
       if (rescale && i > 0) {
         // the output of the tiles before this one, complete, times the factor
-        const int before = st == 0 ? kStages - 1 : st - 1;
+        const int before = st == 0 ? stages - 1 : st - 1;
         ok = mbar_wait<true>(&sh.empty[before][1], st == 0 ? phase ^ 1 : phase, &sh.abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -615,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.weights[i & 1]);
-      if (++st == kStages) {
+      if (++st == stages) {
         st = 0;
         phase ^= 1;
       }
