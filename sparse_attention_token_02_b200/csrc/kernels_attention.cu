@@ -87,6 +87,7 @@ constexpr uint32_t kTmemQ = 384;
 constexpr uint32_t kUpperLanes = 16u << 16;
 
 constexpr int kMaxCluster = 16;                              // parts of a row that a cluster joins
+constexpr int kMaxSlots = 256;                               // and that the second kernel does
 
 constexpr int kSoftmaxWarps = 4;
 constexpr int kFirstWarp = 4, kSecondWarp = 5;                // issue the first and the second products
@@ -775,29 +776,61 @@ __global__ void __launch_bounds__(256) expand_kernel(LatentView kv, int32_t seq,
         __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(kv.rope) + static_cast<int64_t>(row) * kLatentRope) + lane);
 }
 
-// Joins the parts of one row: weights 2^(lse_i - max) over their sum.  128 threads, 4 values each.
-__global__ void __launch_bounds__(128) attention_join_kernel(AttnArgs a, int slots) {
+// Joins the parts of one row: weights 2^(lse_i - max) over their sum, made by a lane per part; then 128 threads add up
+// four values each, eight parts' loads at a time.  Bound by the latency of those loads: rows of many parts get four such
+// groups of threads (128 rows of 74 parts took 14 us with one).
+template <int GROUPS>
+__global__ void __launch_bounds__(GROUPS * 128) attention_join_kernel(AttnArgs a, int slots) {
+  __shared__ float weight[kMaxSlots];
+  __shared__ float part[4 * GROUPS];
+  __shared__ float4 sums[GROUPS][128];
   grid_dependency_wait();
   launch_dependents();
   const int64_t r = blockIdx.x, R = static_cast<int64_t>(a.T) * a.H;
-  float m = -INFINITY;
-  for (int s = 0; s < slots; ++s) m = fmaxf(m, a.part_lse[s * R + r]);
-  const float ref = m == -INFINITY ? 0.f : m;
+  const int tid = threadIdx.x, c = tid & 127, group = tid >> 7;
+  float top = -INFINITY;
+  for (int s = tid; s < slots; s += GROUPS * 128) top = fmaxf(top, weight[s] = a.part_lse[s * R + r]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if ((tid & 31) == 0) part[tid >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4 * GROUPS; ++i) top = fmaxf(top, part[i]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  const float4* v = reinterpret_cast<const float4*>(a.part_o + r * kLatentDim) + c;
   float total = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < slots; ++s) {
-    const float lse = a.part_lse[s * R + r];
-    if (lse == -INFINITY) continue;                      // nothing was written for it
-    const float w = exp2f(lse - ref);
-    const float4 x = *reinterpret_cast<const float4*>(a.part_o + (s * R + r) * kLatentDim + threadIdx.x * 4);
-    total += w;
-    o.x += w * x.x; o.y += w * x.y; o.z += w * x.z; o.w += w * x.w;
+  for (int s0 = group * 8; s0 < slots; s0 += GROUPS * 8) {
+    float4 x[8];
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {                        // 0 past the last part, and where nothing was written
+      w[e] = s0 + e < slots ? exp2f(weight[s0 + e] - ref) : 0.f;
+      x[e] = w[e] != 0.f ? v[(s0 + e) * R * (kLatentDim / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      total += w[e];
+      o.x += w[e] * x[e].x; o.y += w[e] * x[e].y; o.z += w[e] * x[e].z; o.w += w[e] * x[e].w;
+    }
+  }
+  if constexpr (GROUPS > 1) {
+    __syncthreads();                                     // every weight has been read
+    sums[group][c] = o;
+    if (c == 0) weight[group] = total;
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 1; g < GROUPS; ++g) {
+      const float4 x = sums[g][c];
+      o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w;
+      total += weight[g];
+    }
   }
   const float inv = total == 0.f ? 0.f : 1.f / total;
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + r * kLatentDim + threadIdx.x * 4) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-  if (a.lse && threadIdx.x == 0) a.lse[r] = total == 0.f ? -INFINITY : (m + log2f(total)) * kLn2;
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + r * kLatentDim + c * 4) =
+      make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
+  if (a.lse && c == 0) a.lse[r] = total == 0.f ? -INFINITY : (top + log2f(total)) * kLn2;
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -848,11 +881,28 @@ int cluster_room(int cluster, int sms) {
   return room;
 }
 
+// Time until `sms` SMs that take items in order are done with n1 items of cost c1 and then n2 of cost c2.
+double finish(int64_t n1, double c1, int64_t n2, double c2, int64_t sms) {
+  const int64_t ahead = n1 % sms;                        // SMs with one item more than the others
+  const double low = double(n1 / sms) * c1, high = ahead ? low + c1 : low;
+  if (n2 == 0) return high;
+  double lo = std::max(high, low), hi = high + double(ceil_div(n2, sms)) * c2;
+  auto room = [&](double t) { return ahead * int64_t((t - high) / c2 + 1e-9) + (sms - ahead) * int64_t((t - low) / c2 + 1e-9); };
+  if (room(lo) >= n2) return lo;
+  for (int i = 0; i < 20; ++i) {
+    const double t = 0.5 * (lo + hi);
+    (room(t) >= n2 ? hi : lo) = t;
+  }
+  return hi;
+}
+
 // Cuts a call into items, in units of a tile's time.  An item costs its tiles and about four tiles' time beside them
 // (set-up, queries, result).  Splitting a row costs its join: in a cluster (two to sixteen parts) about two more, through
 // memory with a second kernel about five and the parts' traffic.  A token's rows are whole groups where H is a
 // multiple of 64; sharing a prefix then saves no tile, and shared positions are read by the tokens' own items.
-AttnPlan plan_attention(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, bool fp8, int sms) {
+namespace {
+
+AttnPlan make_plan(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, bool fp8, int sms) {
   const int64_t R = T * H, shared_groups = ceil_div(R, kAttnRows), own_groups = ceil_div(H, kAttnRows);
   int64_t shared_tiles = ceil_div(shared_keys, kAttnTile);
   // Expanding FP8 rows to bf16 costs the loading warps more time than a tile's products take; a prefix that many
@@ -876,26 +926,52 @@ AttnPlan plan_attention(int64_t T, int32_t H, int64_t shared_keys, int64_t own_k
     p.shared_chunk = p.own_chunk = static_cast<int32_t>(chunk * kAttnTile);
     p.cluster = cluster;
     p.expand = expand;
-    const int64_t items = shared_groups * p.shared_slots + T * own_groups * p.own_slots;
-    const double join = cluster > 1 ? 2.0 : p.slots() > 1 ? 5.0 + double(p.slots()) * R * 0.0006 : 0.0;
-    const double cost = ceil_div(items, cluster > 1 ? cluster_room(cluster, sms) : sms) * (chunk + 4.0) + join;
+    if (p.slots() > kMaxSlots) return;
+    const double join = cluster > 1 ? 2.0 : p.slots() > 1 ? 5.0 + double(p.slots()) * R * 0.0004 : 0.0;
+    const double cost = join + finish(shared_groups * p.shared_slots, double(chunk) + 4.0, T * own_groups * p.own_slots,
+                                      double(std::min(chunk, own_tiles)) + 4.0, cluster > 1 ? cluster_room(cluster, sms) : sms);
     if (best.slots() == 0 || cost < best_cost) {
       best = p;
       best_cost = cost;
     }
-    return items;
   };
   consider(longest, 1);
   if (shared_tiles == 0)
     for (int cluster = 2; cluster <= kMaxCluster && cluster <= own_tiles; cluster *= 2) consider(ceil_div(own_tiles, cluster), cluster);
+  // chunks with which the longer part fills one to four rounds of the SMs, alone or with the other part beside it
+  const int64_t groups = shared_tiles ? shared_groups : T * own_groups;
   const int64_t tiles = shared_groups * shared_tiles + T * own_groups * own_tiles;
-  for (int waves = 1; waves <= 4; ++waves) {
-    const int64_t room = int64_t(waves) * sms;
-    int64_t chunk = std::min(longest, ceil_div(tiles, room));
-    // rounding up to whole chunks can need more items than fit: grow the chunk until they do
-    while (chunk < longest && consider(chunk, 1) > room) chunk += std::max<int64_t>(1, chunk / 16);
+  for (int rounds = 1; rounds <= 4; ++rounds) {
+    const int64_t pieces = int64_t(rounds) * sms / groups;          // of each group of rows
+    if (pieces > 1) consider(std::max<int64_t>(ceil_div(longest, pieces), ceil_div(longest, kMaxSlots / 2)), 1);
+    // rounding up to whole chunks can need a few items too many: larger chunks need fewer
+    int64_t chunk = std::max(ceil_div(tiles, int64_t(rounds) * sms), ceil_div(longest, kMaxSlots / 2));
+    for (int x = 0; x < 4 && chunk < longest; ++x, chunk += std::max<int64_t>(1, chunk / 16)) consider(chunk, 1);
   }
   return best;
+}
+
+}  // namespace
+
+// The plan depends on the sizes alone; a call and the workspace query before it ask for the same one.
+AttnPlan plan_attention(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, bool fp8, int sms) {
+  struct Last {
+    int64_t T = 0, shared_keys = 0, own_keys = 0;
+    int32_t H = 0, fp8 = 0, sms = 0;
+    AttnPlan plan{};
+  };
+  thread_local Last last;
+  const int32_t wide = fp8 && shared_keys > 0;           // the element type matters to a shared prefix only
+  if (last.T != T || last.H != H || last.shared_keys != shared_keys || last.own_keys != own_keys || last.fp8 != wide || last.sms != sms) {
+    last.plan = make_plan(T, H, shared_keys, own_keys, wide, sms);
+    last.T = T;
+    last.H = H;
+    last.shared_keys = shared_keys;
+    last.own_keys = own_keys;
+    last.fp8 = wide;
+    last.sms = sms;
+  }
+  return last.plan;
 }
 
 namespace {
@@ -952,9 +1028,11 @@ cudaError_t launch_attention(const AttnArgs& args, const AttnPlan& p, int* launc
   ++*launched;
   if (p.parts()) {
     cfg.gridDim = dim3(static_cast<unsigned>(int64_t(a.T) * a.H));
-    cfg.blockDim = dim3(128);
+    const bool many = p.slots() > 16;
+    cfg.blockDim = dim3(many ? 512 : 128);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, attention_join_kernel, a, static_cast<int>(p.slots()));
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, many ? attention_join_kernel<4> : attention_join_kernel<1>, a, static_cast<int>(p.slots()));
     if (e != cudaSuccess) return e;
     ++*launched;
   }
