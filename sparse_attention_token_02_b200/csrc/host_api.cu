@@ -1402,6 +1402,7 @@ dsa_status_t run_attention(const dsa_latent_query_t* q, AttnArgs* a, int64_t sha
   Ctx* c = nullptr;
   dsa_status_t st = get_ctx(stream, &c);
   if (st != DSA_OK) return st;
+  AllowAllocation allow;                               // a kernel's first use may come inside a capture
   const AttnPlan p = plan_attention(q->T, q->H, shared_keys, own_keys, a->kv.fp8, current_sms());
   if ((st = attention_parts(c, attention_workspace(p, q->T, q->H, shared_keys), workspace, workspace_bytes, &a->workspace)) != DSA_OK)
     return st;

@@ -852,14 +852,14 @@ cudaError_t set_up(bool fp8) {
 }
 
 // CTAs that run at once in clusters of a size (2, 4, 8, 16): a cluster's SMs belong to one GPC, so that is fewer than
-// there are SMs.  Without a device (a workspace query on a host that has none): an estimate.
+// there are SMs; 0 where not even one fits.  Without a device (a workspace query on a host that has none): an estimate.
 int cluster_room(int cluster, int sms) {
-  static std::atomic<int> known[64][5];
+  static std::atomic<int> known[64][5];                  // room + 1
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return sms / 18 * 16;
   const int i = __builtin_ctz(cluster);
-  int room = known[dev][i].load(std::memory_order_relaxed);
-  if (room == 0) {
+  int room = known[dev][i].load(std::memory_order_relaxed) - 1;
+  if (room < 0) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
@@ -871,12 +871,12 @@ int cluster_room(int cluster, int sms) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (set_up(false) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, attention_kernel<false>, &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();
-      return sms / 18 * 16;
+    if (set_up(false) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, attention_kernel<false>, &cfg) != cudaSuccess) {
+      cudaGetLastError();                                // asked again next time; clusters stay unused until it answers
+      return 0;
     }
     room = n * cluster;
-    known[dev][i].store(room, std::memory_order_relaxed);
+    known[dev][i].store(room + 1, std::memory_order_relaxed);
   }
   return room;
 }
@@ -926,10 +926,11 @@ AttnPlan make_plan(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, 
     p.shared_chunk = p.own_chunk = static_cast<int32_t>(chunk * kAttnTile);
     p.cluster = cluster;
     p.expand = expand;
-    if (p.slots() > kMaxSlots) return;
+    const int room = cluster > 1 ? cluster_room(cluster, sms) : sms;
+    if (p.slots() > kMaxSlots || room < cluster) return;
     const double join = cluster > 1 ? 2.0 : p.slots() > 1 ? 5.0 + double(p.slots()) * R * 0.0004 : 0.0;
     const double cost = join + finish(shared_groups * p.shared_slots, double(chunk) + 4.0, T * own_groups * p.own_slots,
-                                      double(std::min(chunk, own_tiles)) + 4.0, cluster > 1 ? cluster_room(cluster, sms) : sms);
+                                      double(std::min(chunk, own_tiles)) + 4.0, room);
     if (best.slots() == 0 || cost < best_cost) {
       best = p;
       best_cost = cost;

@@ -449,6 +449,79 @@ def test_prefix_attention_cuts_and_reports_a_length_past_its_bound():
         check_token(f64(out)[t], f64(lse)[t], f64(torch.cat([ql, qr], 2))[t], vals[:n], SM, t)
 
 
+def test_prefix_attention_of_no_keys():
+    cache, _ = make_cache(64, 64, False, 4)
+    table = torch.zeros(3, 1, dtype=torch.int32).cuda()
+    ql, qr = (t.cuda() for t in queries(3, 70, 1))
+    out = torch.full((3, 70, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lens = torch.zeros(3, dtype=torch.int32).cuda()
+    _, lse = api.dsa_prefix_attention(ql, qr, cache, table, lens, lens, SM, max_keys=0, out=out)
+    assert not out.any() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("T,H,prefix,own,hole", [(40, 16, 8000, 30, False), (40, 16, 8000, 30, True), (5, 128, 8100, 0, False)])
+def test_prefix_attention_fp8_prefix_of_many_rows(T, H, prefix, own, hole):
+    # enough rows read the prefix for it to be expanded once; a page that does not exist is left out and reported
+    page = 64
+    full = prefix // page
+    pages = -(-(prefix + own) // page)
+    num_pages = full + T * (pages - full) + 1
+    cache, vals = make_cache(num_pages * page, page, True, T)
+    table = torch.cat([torch.arange(full).expand(T, full), full + torch.arange(T * (pages - full)).view(T, pages - full)], 1).to(torch.int32)
+    if hole:
+        table[0, 3] = -1
+    src = table[0, full].item() * page if prefix % page else 0
+    for t in range(1, T):
+        dst = table[t, full].item() * page if prefix % page else 0
+        for x in (cache.latent, cache.scale, cache.rope):
+            x[dst:dst + prefix % page] = x[src:src + prefix % page].clone()
+        vals[dst:dst + prefix % page] = vals[src:src + prefix % page]
+    lens = torch.full((T,), prefix + own, dtype=torch.int32)
+    lens[1] = prefix + own // 2
+    lens[2] = 100
+    seq = torch.arange(T, dtype=torch.int32)
+    seq[3] = -1
+    ql, qr = queries(T, H, 5)
+    out, lse = api.dsa_prefix_attention(ql.cuda(), qr.cuda(), cache, table.cuda(), seq.cuda(), lens.cuda(), SM, prefix_len=prefix,
+                                        max_keys=prefix + own)
+    if hole:
+        with pytest.raises(RuntimeError, match="DEVICE_CHECK.*page table"):
+            api.dsa_check_device_errors()
+    else:
+        api.dsa_check_device_errors()
+    q = f64(torch.cat([ql, qr], 2))
+    for t in (0, 1, 2, 3, T - 1):
+        n = int(lens[t]) if seq[t] >= 0 else 0
+        rows = [L.page_row(table.numpy(), page, num_pages, 0 if p < prefix else t, p) for p in range(n)]
+        check_token(f64(out)[t], f64(lse)[t], q[t], vals[[r for r in rows if r >= 0]], SM, t)
+
+
+def test_prefix_attention_many_parts():
+    # one token's few heads over a long cache: more parts than the joining kernel's threads take in one round
+    n, page = 70001, 64
+    cache, vals = make_cache(-(-n // page) * page, page, False, 3)
+    table = torch.randperm(-(-n // page), generator=gen(1)).to(torch.int32).view(1, -1)
+    ql, qr = queries(1, 9, 2)
+    lens = torch.tensor([n], dtype=torch.int32)
+    out, lse = api.dsa_prefix_attention(ql.cuda(), qr.cuda(), cache, table.cuda(), torch.zeros(1, dtype=torch.int32).cuda(), lens.cuda(),
+                                        SM, max_keys=n)
+    api.dsa_check_device_errors()
+    rows = (table[0].long()[torch.arange(n) // page] * page + torch.arange(n) % page).numpy()
+    check_token(f64(out)[0], f64(lse)[0], f64(torch.cat([ql, qr], 2))[0], vals[rows], SM, 0)
+
+
+def test_fp8_nan_codes_reach_the_rows_that_read_them():
+    cache, vals = make_cache(128, 64, True, 5)
+    cache.latent[70, 17] = 0x7F
+    cache.latent[71, 300] = 0xFF
+    table = torch.arange(2, dtype=torch.int32).view(1, 2).cuda()
+    ql, qr = queries(3, 12, 3)
+    idx = torch.tensor([[1, 2, 3], [1, 70, 3], [71, -1, 2]], dtype=torch.int32)
+    out, lse = api.dsa_sparse_attention(ql.cuda(), qr.cuda(), cache, table, torch.zeros(3, dtype=torch.int32).cuda(), idx.cuda(), SM)
+    check_token(f64(out)[0], f64(lse)[0], f64(torch.cat([ql, qr], 2))[0], vals[[1, 2, 3]], SM, 0)
+    assert torch.isnan(lse[1:]).all() and torch.isnan(out[1:]).all()
+
+
 # ------------------------------------------------------------------------------------------------ together
 
 
@@ -579,6 +652,28 @@ def test_two_graphs_at_once_and_another_stream():
     assert all(torch.equal(o[0], want[0][0]) for o in outs)
     for s in streams:
         api.dsa_check_device_errors(s)
+
+
+def test_first_calls_on_a_stream_may_be_captured():
+    # a stream the library has not seen: the call's context and its own workspace appear inside the capture
+    cache, vals = make_cache(64 * 64, 64, False, 9)
+    table = torch.arange(64, dtype=torch.int32).view(1, 64).cuda()
+    ids, lens = torch.zeros(40, dtype=torch.int32).cuda(), torch.full((40,), 4096, dtype=torch.int32).cuda()
+    ql, qr = (t.cuda() for t in queries(40, 16, 3))
+    want = api.dsa_prefix_attention(ql, qr, cache, table, ids, lens, SM, prefix_len=3000, max_keys=4096)[0]
+    out = torch.zeros_like(want)
+    lib, side, graph = _lib.load(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    q = _lib.LatentQuery(ql.data_ptr(), ql.stride(0), ql.stride(1), qr.data_ptr(), qr.stride(0), qr.stride(1), 40, 16)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        _lib.check(lib.dsa_prefix_attention(q, cache.c(), _lib.PageTable(table.data_ptr(), 1, 64), ids.data_ptr(), lens.data_ptr(), 3000, 0,
+                                            4096, SM, out.data_ptr(), None, None, 0, side.cuda_stream))
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    api.dsa_check_device_errors(side)
 
 
 def test_selection_of_everything_is_dense_attention():
