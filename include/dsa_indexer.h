@@ -461,7 +461,7 @@ typedef struct {
  * A token with no entry, or with a negative sequence (padding), gets zeros and -inf.  Scores, softmax
  * statistics and sums are fp32; the weights are rounded to bf16 for their product with the latents.  The
  * result is the same, bit for bit, on every run.
- *   workspace  device, 256-byte aligned, dsa_sparse_attention_workspace_bytes(T, H, top_k) bytes (which may
+ *   workspace  device, 256-byte aligned, dsa_sparse_attention_workspace_bytes() bytes (which may
  *              be 0), used until the call's kernels finish; or NULL for the stream's own, grown with
  *              cudaMalloc (graphs captured with NULL on one stream share it and must not run at the same
  *              time).  dsa_set_workspace does not apply here.
@@ -489,7 +489,7 @@ DSA_API dsa_status_t dsa_prefix_attention(const dsa_latent_query_t* q, const dsa
                                           size_t workspace_bytes, void* stream);
 
 /* Workspace bytes of the two attention calls on the current device (0: none needed); dtype: the cache's. */
-DSA_API size_t dsa_sparse_attention_workspace_bytes(int32_t T, int32_t H, int32_t top_k);
+DSA_API size_t dsa_sparse_attention_workspace_bytes(int32_t T, int32_t H, int32_t top_k, dsa_dtype_t dtype);
 DSA_API size_t dsa_prefix_attention_workspace_bytes(int32_t T, int32_t H, int32_t prefix_len, int32_t max_keys,
                                                     dsa_dtype_t dtype);
 

@@ -151,7 +151,7 @@ def load() -> ctypes.CDLL:
     lib.dsa_prefix_attention.argtypes = [P(LatentQuery), P(LatentCacheView), P(PageTable), V, V, I32, I32, I32, F32, V,
                                          V, V, ctypes.c_size_t, V]
     lib.dsa_prefix_attention.restype = st
-    lib.dsa_sparse_attention_workspace_bytes.argtypes = [I32, I32, I32]
+    lib.dsa_sparse_attention_workspace_bytes.argtypes = [I32, I32, I32, ctypes.c_int]
     lib.dsa_sparse_attention_workspace_bytes.restype = ctypes.c_size_t
     lib.dsa_prefix_attention_workspace_bytes.argtypes = [I32, I32, I32, I32, ctypes.c_int]
     lib.dsa_prefix_attention_workspace_bytes.restype = ctypes.c_size_t

@@ -382,6 +382,10 @@ class LatentCache:
     def fp8(self) -> bool:
         return self.latent.dtype in (torch.uint8, torch.float8_e4m3fn)
 
+    @property
+    def code(self) -> int:
+        return DSA_BF16 if self.latent.dtype is torch.bfloat16 else DSA_FP8_E4M3
+
     def c(self) -> _lib.LatentCacheView:
         latent, rope, scale, page_size = self.latent, self.rope, self.scale, self.page_size
         rows, d_c = latent.shape
@@ -573,7 +577,7 @@ def dsa_sparse_attention(q_latent, q_rope, cache: LatentCache, page_table, seq_i
         with guard:
             return dsa_sparse_attention(q_latent, q_rope, cache, page_table, seq_ids, idx, sm_scale, out, lse, workspace)
     lib = _lib.load()
-    need = lib.dsa_sparse_attention_workspace_bytes(T, H, k) if workspace is None else 0
+    need = 0 if workspace is not None else lib.dsa_sparse_attention_workspace_bytes(T, H, k, cache.code)
     out, lse, workspace, given = _outputs(T, H, q_latent, out, lse, workspace, need)
     _one_device(q_latent, cache.latent, cache.rope, cache.scale, page_table, seq_ids, idx, out, lse, workspace)
     _one_device(q_latent, q_rope, contiguous=False)
@@ -600,8 +604,7 @@ def dsa_prefix_attention(q_latent, q_rope, cache: LatentCache, page_table, seq_i
     if max_keys is None:
         max_keys = table.max_pages * cache.page_size
     lib = _lib.load()
-    need = 0 if workspace is not None else lib.dsa_prefix_attention_workspace_bytes(
-        T, H, prefix_len, max_keys, DSA_BF16 if cache.latent.dtype is torch.bfloat16 else DSA_FP8_E4M3)
+    need = 0 if workspace is not None else lib.dsa_prefix_attention_workspace_bytes(T, H, prefix_len, max_keys, cache.code)
     out, lse, workspace, given = _outputs(T, H, q_latent, out, lse, workspace, need)
     _one_device(q_latent, cache.latent, cache.rope, cache.scale, page_table, seq_ids, key_lens, out, lse, workspace)
     _one_device(q_latent, q_rope, contiguous=False)
@@ -611,8 +614,8 @@ def dsa_prefix_attention(q_latent, q_rope, cache: LatentCache, page_table, seq_i
     return out, lse
 
 
-def dsa_sparse_attention_workspace_bytes(T: int, H: int, top_k: int) -> int:
-    return int(_lib.load().dsa_sparse_attention_workspace_bytes(T, H, top_k))
+def dsa_sparse_attention_workspace_bytes(T: int, H: int, top_k: int, fp8: bool = False) -> int:
+    return int(_lib.load().dsa_sparse_attention_workspace_bytes(T, H, top_k, DSA_FP8_E4M3 if fp8 else DSA_BF16))
 
 
 def dsa_prefix_attention_workspace_bytes(T: int, H: int, prefix_len: int, max_keys: int, fp8: bool = False) -> int:

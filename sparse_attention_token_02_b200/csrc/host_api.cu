@@ -1540,9 +1540,9 @@ dsa_status_t dsa_prefix_attention(const dsa_latent_query_t* q, const dsa_latent_
   return run_attention(q, &a, prefix_len, max_keys - prefix_len, sm_scale, out, lse, workspace, workspace_bytes, stream_v);
 }
 
-size_t dsa_sparse_attention_workspace_bytes(int32_t T, int32_t H, int32_t top_k) {
+size_t dsa_sparse_attention_workspace_bytes(int32_t T, int32_t H, int32_t top_k, dsa_dtype_t dtype) {
   if (T < 1 || H < 1 || H > 128 || top_k < 1 || top_k > kMaxKeys) return 0;
-  return attention_workspace(plan_attention(T, H, 0, top_k, false, current_sms()), T, H, 0);
+  return attention_workspace(plan_attention(T, H, 0, top_k, dtype == DSA_FP8_E4M3, current_sms()), T, H, 0);
 }
 
 size_t dsa_prefix_attention_workspace_bytes(int32_t T, int32_t H, int32_t prefix_len, int32_t max_keys, dsa_dtype_t dtype) {

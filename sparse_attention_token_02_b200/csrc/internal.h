@@ -218,6 +218,7 @@ struct AttnPlan {
   int32_t shared_groups, shared_slots, shared_chunk;
   int32_t own_groups, own_slots, own_chunk;       // own_groups: row groups of one token
   int32_t cluster;                                // > 1: the own_slots CTAs of a row group are a cluster and join their parts there
+  int32_t pair;                                   // pairs of CTAs, each pair against two groups of rows
   int32_t expand;                                 // the shared prefix of an FP8 cache goes to bf16 first
   __host__ __device__ bool parts() const { return cluster == 1 && slots() > 1; }   // parts go to memory
   __host__ __device__ int32_t slots() const { return shared_slots + own_slots; }
@@ -237,6 +238,7 @@ struct AttnArgs {
   int32_t shared_len, shared_seq;   // positions [0, shared_len) are read through sequence shared_seq
   int32_t max_keys;            // bound on key_lens
   float scale_log2;            // softmax scale * log2(e)
+  int32_t first_item;          // items before it are left out
   void* out;                   // [T, H, 512] bf16
   float* lse;                  // [T, H] or nullptr
   float* part_o;               // [slots, T * H, 512] (slots > 1)

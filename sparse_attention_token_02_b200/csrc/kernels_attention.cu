@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
 
   // the item
   const int n_shared = p.shared_groups * p.shared_slots;
-  int item = blockIdx.x;
+  int item = blockIdx.x + a.first_item;
   int row0;                      // first of the item's rows in the packed [T, H]
   int rows, slot, token = -1;
   if (p.cluster > 1) {
@@ -752,6 +752,500 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
   }
 }
 
+// ------------------------------------------------------------------------------------------------ the pass, in pairs
+//
+// Two CTAs (a cluster) take 128 rows, 64 each, against the same keys: products of 128 rows over a pair of SMs run at the
+// tensor cores' full rate, where 64 rows on one run at half.  For the scores a CTA holds half of a tile's keys (32 rows
+// of 576 values), for the second product half of the values of all its keys (64 rows of 256).  Keys and values have
+// their own stages: a tile's keys are free after its scores, its values after the second product.  CTA 0 issues; CTA 1's
+// two idle warps tell it when their CTA's keys and values have landed.  (64 x 128 heads over 2048 selected keys 69 -> 58
+// us, 512 tokens 805 -> 703.)  A tile takes about 1800 cycles: 1280 of products, about 1500 of shared memory (operands
+// 860, copies in 540, weights 100).  Copying the values of a CTA's own keys from its keys' stage, which spares a quarter
+// of the reads of L2, cost 743 us for the 703.
+constexpr uint32_t kPairKeys = (kLatentBlocks + 1) * 4096u;  // 32 rows x 9 blocks
+constexpr uint32_t kPairValues = 4 * kBlock;                 // 64 rows x 4 blocks
+constexpr int kKeyStages = 2, kValueStages = 3;
+constexpr int kPairQBlocks = 3;                              // the queries' values 384 .. 511 and rotated part
+constexpr uint32_t kPairP = kPairQBlocks * kBlock;           // two tiles' weights
+constexpr uint32_t kPairK = kPairP + 2 * kBlock;
+constexpr uint32_t kPairV = kPairK + kKeyStages * kPairKeys;
+constexpr uint32_t kPairSmem = kPairV + kValueStages * kPairValues;
+static_assert(64 * kOutRow32 <= kPairSmem - kPairK, "the result must fit");
+// tensor memory: the output (two products of 256 values, 128 columns each), two score tiles, the queries' values 0 .. 383
+constexpr uint32_t kPairTmemS = 256;
+constexpr uint32_t kPairTmemQ = 320;
+
+struct __align__(8) SharedPair {
+  uint64_t keys[kKeyStages], values[kValueStages];           // this CTA's copies have landed
+  uint64_t peer_keys[kKeyStages], peer_values[kValueStages]; // CTA 0's: and CTA 1's
+  uint64_t scores[2];           // a score tile is complete, its keys' stage free
+  uint64_t used[kValueStages];  // the tile's second product is done
+  uint64_t taken[2], weights[2];   // CTA 0's: both CTAs have read the scores, have written the weights
+  uint64_t listed[kValueStages];
+  uint64_t queries;             // CTA 0's
+  uint64_t drained[2];
+  uint32_t tmem;
+  int abort;
+  int32_t key_end;
+  int32_t limit[kAttnRows];
+  float inv[kAttnRows];
+  float top[2][2][kAttnRows];   // a tile's maxima over either half of its keys, two tiles in turn
+  alignas(8) uint8_t valid[kValueStages][2][kLoadWarps];   // keys that exist, four bits a warp and half
+};
+
+__global__ void __launch_bounds__(kThreads, 1) attention_pair_kernel(AttnArgs a, AttnPlan p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ SharedPair sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t smem = smem_addr(smem_raw);
+  const int rank = static_cast<int>(cluster_rank());
+
+  // the item: the same keys for both CTAs
+  const int pairs = (p.shared_groups + 1) / 2;
+  int item = blockIdx.x >> 1;
+  int pair0, row0, rows, slot, token = -1;   // first row of the pair's, of this CTA's rows
+  int32_t k0, k1;
+  if (item < pairs * p.shared_slots) {
+    pair0 = item % pairs * 2 * kAttnRows;
+    row0 = pair0 + rank * kAttnRows;
+    rows = max(0, min(kAttnRows, a.T * a.H - row0));
+    slot = item / pairs;
+    k0 = slot * p.shared_chunk;
+    k1 = min(k0 + p.shared_chunk, a.shared_len);
+  } else {
+    item -= pairs * p.shared_slots;
+    token = item % a.T;
+    slot = p.shared_slots + item / a.T;
+    pair0 = token * a.H;
+    row0 = pair0 + rank * kAttnRows;
+    rows = max(0, min(kAttnRows, a.H - rank * kAttnRows));
+    k0 = (p.shared_slots ? a.shared_len : 0) + (slot - p.shared_slots) * p.own_chunk;
+    k1 = min(k0 + p.own_chunk, a.idx ? a.top_k : a.max_keys);
+  }
+  const LatentView& kv = token < 0 ? a.shared : a.kv;
+  const bool rotated = a.kv.rope != nullptr;
+
+  if (warp == kFirstWarp) {
+    if (lane == 0) {
+      for (int i = 0; i < kKeyStages; ++i) {
+        mbar_init(&sh.keys[i], kLoadWarps * 32);
+        mbar_init(&sh.peer_keys[i], 1);
+      }
+      for (int i = 0; i < kValueStages; ++i) {
+        mbar_init(&sh.values[i], kLoadWarps * 32);
+        mbar_init(&sh.peer_values[i], 1);
+        mbar_init(&sh.used[i], 1);
+        mbar_init(&sh.listed[i], kLoadWarps);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sh.scores[i], 1);
+        mbar_init(&sh.taken[i], 2 * kSoftmaxWarps);
+        mbar_init(&sh.weights[i], 2 * kSoftmaxWarps);
+        mbar_init(&sh.drained[i], 1);
+      }
+      mbar_init(&sh.queries, 2 * kSoftmaxWarps);
+      sh.abort = 0;
+      sh.key_end = 0;
+      fence_barrier_init();
+    }
+    __syncwarp();
+    tmem_alloc_pair(&sh.tmem, kTmemCols);
+  }
+  __syncthreads();
+  cluster_arrive();                                      // either's barriers stand before the other arrives there
+  cluster_wait();
+  grid_dependency_wait();
+
+  const int32_t* idx = a.idx ? a.idx + static_cast<int64_t>(token) * a.top_k : nullptr;
+  const int32_t shared_seq = p.expand ? 0 : a.shared_seq;
+  int32_t seq = shared_seq;
+  if (token < 0) {
+    if (tid < 2 * kAttnRows) {                           // both CTAs' rows: they stop at the same key
+      int32_t n = 0;
+      if (pair0 + tid < a.T * a.H) {
+        const int32_t t = (pair0 + tid) / a.H;
+        n = token_limit(a, t, token_seq(a, t));
+      }
+      if (tid / kAttnRows == rank) sh.limit[tid % kAttnRows] = n;
+      atomicMax(&sh.key_end, min(n, k1));
+    }
+  } else {
+    seq = token_seq(a, token);
+    if (idx == nullptr) {
+      const int32_t n = token_limit(a, token, seq);
+      if (tid < kAttnRows) sh.limit[tid] = n;
+      if (tid == 0) sh.key_end = min(n, k1);
+    } else {
+      if (tid < kAttnRows) sh.limit[tid] = 0x7FFFFFFF;
+      int32_t last = 0;
+      for (int32_t k = k0 + tid; k < k1; k += 8 * kThreads) {
+        int32_t e[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) e[x] = k + x * kThreads < k1 ? __ldg(idx + k + x * kThreads) : -1;
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          if (e[x] >= 0) last = k + x * kThreads + 1;
+      }
+      last = __reduce_max_sync(0xffffffffu, seq < 0 ? 0 : last);
+      if (lane == 0 && last > 0) atomicMax(&sh.key_end, last);
+    }
+  }
+  __syncthreads();
+  const int32_t key_end = sh.key_end;
+  const int tiles = key_end > k0 ? (key_end - k0 + kAttnTile - 1) / kAttnTile : 0;
+  tc_fence_after();
+
+  if (warp >= kLoadWarp0) {
+    // ---------------------------------------------------------------- loads
+    const int lw = warp - kLoadWarp0;
+    const int sub = lane >> 3, col = lane & 7;
+    if (tiles > 0) {
+#pragma unroll 1
+      for (int r = lw * 8 + sub; r < lw * 8 + 8; r += 4) {   // the queries' share of shared memory, wanted with the first keys
+        const int qr = row0 + (r < rows ? r : 0);
+        const int t = rows > 0 ? qr / a.H : 0, h = rows > 0 ? qr - t * a.H : 0;
+        const uint32_t dst = smem + r * 128 + ((col ^ (r & 7)) << 4);
+        const __nv_bfloat16* ql = static_cast<const __nv_bfloat16*>(a.q_latent) + t * a.ql_t + h * a.ql_h + 384 + col * 8;
+        cp_async16(dst, ql, r < rows);
+        cp_async16(dst + kBlock, ql + 64, r < rows);
+        if (rotated)
+          cp_async16(dst + 2 * kBlock, static_cast<const __nv_bfloat16*>(a.q_rope) + t * a.qr_t + h * a.qr_h + col * 8, r < rows);
+      }
+    }
+    // The warp's eight keys of a tile: four of this CTA's half (columns 0 .. 3) and four of the other's.
+    const int key = (col < 4 ? rank : 1 - rank) * 32 + lw * 4 + (col & 3);
+    int32_t pos2 = -1, pos1 = -1, page1 = -1, row = -1;
+    auto advance = [&](int n) {
+      row = pos1 < 0 ? -1 : page_row(kv, page1, pos1, a.err, token < 0 ? row0 / a.H : token);
+      page1 = pos2 < 0 ? -1 : page_entry(kv, pos2 < a.shared_len ? shared_seq : seq, pos2);
+      pos1 = pos2;
+      const int32_t k = k0 + n * kAttnTile + key;
+      pos2 = k < key_end ? (idx ? __ldg(idx + k) : k) : -1;
+    };
+    int ks = 0, vs = 0;
+    uint32_t kphase = 1, vphase = 1;                     // the stages start free
+    for (int n = 0; n < tiles + 2; ++n) {
+      advance(n);                                        // the rows of tile n - 2
+      if (n < 2) continue;
+      const uint32_t valid = __ballot_sync(0xffffffffu, row >= 0);
+      // keys: row lw * 4 + sub of this CTA's 32
+      bool ok = mbar_wait<true>(&sh.scores[ks], kphase, &sh.abort);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const int32_t rk = __shfl_sync(0xffffffffu, row, sub);
+      const __nv_bfloat16* sk = static_cast<const __nv_bfloat16*>(kv.latent) + static_cast<int64_t>(max(rk, 0)) * kLatentDim + col * 8;
+      const int r32 = lw * 4 + sub;
+      const uint32_t dk = smem + kPairK + ks * kPairKeys + r32 * 128 + ((col ^ (r32 & 7)) << 4);
+#pragma unroll
+      for (int c = 0; c < kLatentBlocks; ++c) cp_async16(dk + c * 4096, sk + c * 64, rk >= 0);
+      if (rotated)
+        cp_async16(dk + kLatentBlocks * 4096, static_cast<const __nv_bfloat16*>(kv.rope) + static_cast<int64_t>(max(rk, 0)) * kLatentRope + col * 8, rk >= 0);
+      cp_async_arrive(&sh.keys[ks]);
+      // values: the rows of the warp's eight keys, this CTA's half of the values
+      ok = mbar_wait<true>(&sh.used[vs], vphase, &sh.abort);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (lane == 0) {
+        sh.valid[vs][rank][lw] = valid & 15;
+        sh.valid[vs][1 - rank][lw] = (valid >> 4) & 15;
+        mbar_arrive(&sh.listed[vs]);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int32_t rv = __shfl_sync(0xffffffffu, row, sub + 4 * j);
+        const int r64 = (j == 0 ? rank : 1 - rank) * 32 + lw * 4 + sub;
+        const __nv_bfloat16* sv = static_cast<const __nv_bfloat16*>(kv.latent) + static_cast<int64_t>(max(rv, 0)) * kLatentDim + rank * 256 + col * 8;
+        const uint32_t dv = smem + kPairV + vs * kPairValues + r64 * 128 + ((col ^ (r64 & 7)) << 4);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) cp_async16(dv + c * kBlock, sv + c * 64, rv >= 0);
+      }
+      cp_async_arrive(&sh.values[vs]);
+      if (++ks == kKeyStages) {
+        ks = 0;
+        kphase ^= 1;
+      }
+      if (++vs == kValueStages) {
+        vs = 0;
+        vphase ^= 1;
+      }
+    }
+    cp_async_wait_all();
+  } else if (warp == kFirstWarp) {
+    if (elect_one()) {
+      bool ok = true;
+      if (rank == 0) {
+        // ---------------------------------------------------------------- scores = Q K^T
+        constexpr uint32_t idesc = make_idesc(1, 2 * kAttnRows, kAttnTile);
+        ok = tiles == 0 || mbar_wait<true>(&sh.queries, 0, &sh.abort);
+        for (int i = 0; i < tiles && ok; ++i) {
+          const int st = i & 1;
+          const uint32_t phase = (i >> 1) & 1;
+          if (i >= 2) ok = mbar_wait<true>(&sh.taken[st], phase ^ 1, &sh.abort);
+          ok = ok && mbar_wait<true>(&sh.keys[st], phase, &sh.abort) && mbar_wait<true>(&sh.peer_keys[st], phase, &sh.abort);
+          if (!ok) break;
+          fence_proxy_async_smem();
+          tc_fence_after();
+          const uint32_t keys = smem + kPairK + st * kPairKeys;
+          const uint32_t d = kPairTmemS + st * 32;
+#pragma unroll
+          for (int ks = 0; ks < 24; ++ks)
+            umma_pair_f16_ts(d, kPairTmemQ + ks * 8, sdesc_kmajor_sw128(keys + (ks >> 2) * 4096 + (ks & 3) * 32), idesc, ks > 0);
+#pragma unroll
+          for (int ks = 24; ks < 32; ++ks)
+            umma_pair_f16(d, sdesc_kmajor_sw128(smem + ((ks - 24) >> 2) * kBlock + (ks & 3) * 32),
+                          sdesc_kmajor_sw128(keys + (ks >> 2) * 4096 + (ks & 3) * 32), idesc, 1);
+          if (rotated) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              umma_pair_f16(d, sdesc_kmajor_sw128(smem + 2 * kBlock + ks * 32),
+                            sdesc_kmajor_sw128(keys + kLatentBlocks * 4096 + ks * 32), idesc, 1);
+          }
+          umma_pair_commit(&sh.scores[st]);
+        }
+        umma_pair_commit(&sh.drained[0]);
+      } else {
+        for (int i = 0; i < tiles && ok; ++i) {
+          ok = mbar_wait<true>(&sh.keys[i & 1], (i >> 1) & 1, &sh.abort);
+          if (!ok) break;
+          fence_proxy_async_smem();                      // the copies that the barrier reported
+          mbar_arrive_cluster(&sh.peer_keys[i & 1], 0);
+        }
+      }
+      int alone = 0;
+      mbar_wait<true>(&sh.drained[0], 0, &alone);
+    }
+    __syncwarp();
+  } else if (warp == kSecondWarp) {
+    if (elect_one()) {
+      bool ok = true;
+      int st = 0;
+      uint32_t phase = 0;
+      if (rank == 0) {
+        // ---------------------------------------------------------------- output += P V
+        constexpr uint32_t idesc = make_idesc(1, 2 * kAttnRows, 256) | kIdescBMnMajor;
+        for (int i = 0; i < tiles; ++i) {
+          ok = mbar_wait<true>(&sh.values[st], phase, &sh.abort) && mbar_wait<true>(&sh.peer_values[st], phase, &sh.abort) &&
+               mbar_wait<true>(&sh.weights[i & 1], (i >> 1) & 1, &sh.abort);
+          if (!ok) break;
+          fence_proxy_async_smem();
+          tc_fence_after();
+          const uint32_t values = smem + kPairV + st * kPairValues, w = smem + kPairP + (i & 1) * kBlock;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int ks = 0; ks < kAttnTile / 16; ++ks)
+              umma_pair_f16(kTmemO + j * 128, sdesc_kmajor_sw128(w + ks * 32),
+                            sdesc_mnmajor_sw128(values + j * 2 * kBlock + ks * 2048, kBlock), idesc, i > 0 || ks > 0);
+          umma_pair_commit(&sh.used[st]);
+          if (++st == kValueStages) {
+            st = 0;
+            phase ^= 1;
+          }
+        }
+        umma_pair_commit(&sh.drained[1]);
+      } else {
+        for (int i = 0; i < tiles; ++i) {
+          ok = mbar_wait<true>(&sh.values[st], phase, &sh.abort);
+          if (!ok) break;
+          fence_proxy_async_smem();
+          mbar_arrive_cluster(&sh.peer_values[st], 0);
+          if (++st == kValueStages) {
+            st = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      int alone = 0;
+      mbar_wait<true>(&sh.drained[1], 0, &alone);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- weights
+    // A thread's row and half of the tile's keys; the warp two further on has the rows' other half.
+    const int r = tid & 63, half = tid >> 6;
+    const int32_t limit = sh.limit[r];
+    const uint32_t quadrant = static_cast<uint32_t>(warp * 32) << 16;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    if (tiles > 0) {
+      const int qr = row0 + (r < rows ? r : 0);
+      const int t = rows > 0 ? qr / a.H : 0, h = rows > 0 ? qr - t * a.H : 0;
+      const uint4* ql = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_latent) + t * a.ql_t + h * a.ql_h);
+#pragma unroll 1
+      for (int c = 0; c < 192; c += 64) {
+        uint4 x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = r < rows ? __ldg(ql + c / 4 + e) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          uint32_t v[32];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[4 * e] = x[8 * y + e].x; v[4 * e + 1] = x[8 * y + e].y; v[4 * e + 2] = x[8 * y + e].z; v[4 * e + 3] = x[8 * y + e].w;
+          }
+          tmem_st_32x32b_x32(quadrant + kPairTmemQ + c + 32 * y, v);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(&sh.queries, 0);
+    }
+    int st = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < tiles; ++i) {
+      const int b = i & 1;
+      ok = ok && mbar_wait<true>(&sh.scores[b], (i >> 1) & 1, &sh.abort) && mbar_wait<true>(&sh.listed[st], phase, &sh.abort);
+      // the weights' place: the second product of the tile before last
+      if (ok && i >= 2) ok = mbar_wait<true>(&sh.used[(i - 2) % kValueStages], ((i - 2) / kValueStages) & 1, &sh.abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {                                         // the partner may be waiting: the barrier of every tile is kept
+        named_barrier(1 + (warp & 1), 64);
+        continue;
+      }
+      tc_fence_after();
+      uint32_t raw[32];
+      tmem_ld_32x32b_x32(quadrant + kPairTmemS + b * 32, raw);
+      uint64_t present = *reinterpret_cast<const uint64_t*>(sh.valid[st][half]);
+      present = (present | present >> 4) & 0x00FF00FF00FF00FFull;         // four bits of every byte, together
+      present = (present | present >> 8) & 0x0000FFFF0000FFFFull;
+      uint32_t mine = static_cast<uint32_t>(present | present >> 16);
+      const int32_t n = limit - (k0 + i * kAttnTile + half * 32);          // the row's keys of this half
+      if (n < 32) mine = n <= 0 ? 0u : mine & ((1u << n) - 1);
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(&sh.taken[b], 0);
+      float x[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(raw[e]);
+      if (!__all_sync(0xffffffffu, mine == 0xFFFFFFFFu)) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (!((mine >> e) & 1)) x[e] = -INFINITY;
+      }
+      float mx = x[0];
+#pragma unroll
+      for (int e = 1; e < 32; ++e) mx = fmaxf(mx, x[e]);
+      sh.top[b][half][r] = mx;
+      named_barrier(1 + (warp & 1), 64);
+      mx = fmaxf(mx, sh.top[b][1 - half][r]) * a.scale_log2;
+      // both warps of a row see the same numbers and decide alike
+      const bool rescale = __any_sync(0xffffffffu, mx > m + kLag);
+      float factor = 1.f;
+      if (rescale) {
+        const float mn = fmaxf(m, mx);
+        factor = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
+        l *= factor;
+        m = mn;
+      }
+      const float ref = m == -INFINITY ? 0.f : m;
+      const uint32_t place = smem + kPairP + b * kBlock + r * 128;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float lo = exp2_fast(fmaf(x[8 * c + 2 * e], a.scale_log2, -ref)), hi = exp2_fast(fmaf(x[8 * c + 2 * e + 1], a.scale_log2, -ref));
+          l += lo + hi;                                  // the sum keeps fp32; the product's operand is bf16
+          w[e] = bf16x2(lo, hi);
+        }
+        st_shared16(place + (((half * 4 + c) ^ (r & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+      }
+      if (rescale && i > 0) {
+        ok = mbar_wait<true>(&sh.used[(i - 1) % kValueStages], ((i - 1) / kValueStages) & 1, &sh.abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) continue;
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 256; c += 32) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(quadrant + kTmemO + c, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+          tmem_st_32x32b_x32(quadrant + kTmemO + c, o);
+        }
+        tmem_st_wait();
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(&sh.weights[b], 0);
+      if (++st == kValueStages) {
+        st = 0;
+        phase ^= 1;
+      }
+    }
+    // the two halves' sums
+    named_barrier(1 + (warp & 1), 64);                   // the last maxima have been read
+    sh.top[0][half][r] = l;
+    named_barrier(1 + (warp & 1), 64);
+    l += sh.top[0][1 - half][r];
+    if (half == 0 && ok) {
+      sh.inv[r] = l == 0.f ? 0.f : 1.f / l;
+      const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+      if (r < rows) {
+        if (p.parts()) a.part_lse[static_cast<int64_t>(slot) * a.T * a.H + row0 + r] = lse2;
+        else if (a.lse) a.lse[row0 + r] = lse2 * kLn2;
+      }
+    }
+  }
+
+  // ---------------------------------------------------------------- the result
+  launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();                                      // both CTAs' copies and products are done
+  cluster_wait();
+  tc_fence_after();
+  const bool wide = p.parts();
+  if (*const_cast<volatile int*>(&sh.abort) != 0) {
+    if (tid == 0) record_error(a.err, DSA_DEVERR_TIMEOUT, static_cast<int>(blockIdx.x));
+  } else if (tiles > 0 || !wide) {
+    const uint32_t stride = wide ? kOutRow32 : kOutRow16;
+    if (warp < 12) {
+      const int r = (warp & 1) * 32 + lane, half = (warp >> 1) & 1;
+      const float inv = sh.inv[r];
+      const uint32_t mem = smem + kPairK + r * stride + half * (wide ? 1024 : 512);
+#pragma unroll 1
+      for (int c = (warp >> 2) * 16; c < 256; c += 48) {
+        uint32_t o[16];
+        tmem_ld_32x32b_x16((static_cast<uint32_t>((warp & 3) * 32) << 16) + kTmemO + c, o);
+        tmem_ld_wait();
+        float val[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) val[e] = inv == 0.f ? 0.f : __uint_as_float(o[e]) * inv;
+        if (wide) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            st_shared16(mem + (c + e) * 4, make_uint4(__float_as_uint(val[e]), __float_as_uint(val[e + 1]),
+                                                      __float_as_uint(val[e + 2]), __float_as_uint(val[e + 3])));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; e += 8)
+            st_shared16(mem + (c + e) * 2, make_uint4(bf16x2(val[e], val[e + 1]), bf16x2(val[e + 2], val[e + 3]),
+                                                      bf16x2(val[e + 4], val[e + 5]), bf16x2(val[e + 6], val[e + 7])));
+        }
+      }
+    }
+    tc_fence_before();
+    __syncthreads();
+    const int shift = wide ? 7 : 6;
+    uint4* out = wide ? reinterpret_cast<uint4*>(a.part_o) + ((static_cast<int64_t>(slot) * a.T * a.H + row0) << shift)
+                      : static_cast<uint4*>(a.out) + (static_cast<int64_t>(row0) << shift);
+#pragma unroll 2
+    for (int v = tid; v < rows << shift; v += kThreads)
+      out[v] = ld_shared16(smem + kPairK + (v >> shift) * stride + (v & ((1 << shift) - 1)) * 16);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();                                      // the pair gives its tensor memory back together
+  cluster_wait();
+  if (warp == kFirstWarp) {
+    tc_fence_after();
+    tmem_dealloc_pair(sh.tmem, kTmemCols);
+  }
+}
+
 // The shared prefix of an FP8 cache in bf16, one row per position, for the many groups of rows that read it: map[p] is p,
 // or -1 where the page table has no page.  One warp per position.
 __global__ void __launch_bounds__(256) expand_kernel(LatentView kv, int32_t seq, int32_t n, __nv_bfloat16* latent,
@@ -847,6 +1341,7 @@ cudaError_t set_up(bool fp8) {
   auto kernel = fp8 ? attention_kernel<true> : attention_kernel<false>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(attention_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
   if (e == cudaSuccess) ready[fp8].fetch_or(bit, std::memory_order_relaxed);
   return e;
 }
@@ -917,8 +1412,9 @@ AttnPlan make_plan(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, 
   const int64_t longest = std::max(shared_tiles, own_tiles);
   AttnPlan best{};
   double best_cost = 0.0;
-  auto consider = [&](int64_t chunk, int cluster) {
+  auto consider = [&](int64_t chunk, int cluster, bool pair = false) {
     AttnPlan p{};
+    p.pair = pair;
     p.shared_groups = static_cast<int32_t>(shared_groups);
     p.own_groups = static_cast<int32_t>(own_groups);
     p.shared_slots = static_cast<int32_t>(ceil_div(shared_tiles, chunk));
@@ -929,7 +1425,15 @@ AttnPlan make_plan(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, 
     const int room = cluster > 1 ? cluster_room(cluster, sms) : sms;
     if (p.slots() > kMaxSlots || room < cluster) return;
     const double join = cluster > 1 ? 2.0 : p.slots() > 1 ? 5.0 + double(p.slots()) * R * 0.0004 : 0.0;
-    const double cost = join + finish(shared_groups * p.shared_slots, double(chunk) + 4.0, T * own_groups * p.own_slots,
+    double cost = join;
+    if (pair) {
+      // two SMs an item; an FP8 cache's own items stay with the single kernel, launched behind
+      const double tile = 0.68;
+      const int64_t shared_pairs = (shared_groups + 1) / 2 * p.shared_slots, own_pairs = fp8 ? 0 : T * p.own_slots;
+      cost += finish(shared_pairs, double(chunk) * tile + 4.5, own_pairs, double(std::min(chunk, own_tiles)) * tile + 4.5, cluster_room(2, sms) / 2);
+      if (fp8 && p.own_slots) cost += 1.0 + finish(T * own_groups * p.own_slots, double(std::min(chunk, own_tiles)) + 4.0, 0, 1.0, sms);
+    } else
+      cost += finish(shared_groups * p.shared_slots, double(chunk) + 4.0, T * own_groups * p.own_slots,
                                       double(std::min(chunk, own_tiles)) + 4.0, room);
     if (best.slots() == 0 || cost < best_cost) {
       best = p;
@@ -937,17 +1441,25 @@ AttnPlan make_plan(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, 
     }
   };
   consider(longest, 1);
+  // in pairs: bf16 keys that at least two groups of rows share
+  const bool pairs = (fp8 ? expand : shared_tiles > 0 || own_groups == 2) && cluster_room(2, sms) >= 2;
+  if (pairs) consider(longest, 1, true);
   if (shared_tiles == 0)
     for (int cluster = 2; cluster <= kMaxCluster && cluster <= own_tiles; cluster *= 2) consider(ceil_div(own_tiles, cluster), cluster);
   // chunks with which the longer part fills one to four rounds of the SMs, alone or with the other part beside it
-  const int64_t groups = shared_tiles ? shared_groups : T * own_groups;
-  const int64_t tiles = shared_groups * shared_tiles + T * own_groups * own_tiles;
-  for (int rounds = 1; rounds <= 4; ++rounds) {
-    const int64_t pieces = int64_t(rounds) * sms / groups;          // of each group of rows
-    if (pieces > 1) consider(std::max<int64_t>(ceil_div(longest, pieces), ceil_div(longest, kMaxSlots / 2)), 1);
-    // rounding up to whole chunks can need a few items too many: larger chunks need fewer
-    int64_t chunk = std::max(ceil_div(tiles, int64_t(rounds) * sms), ceil_div(longest, kMaxSlots / 2));
-    for (int x = 0; x < 4 && chunk < longest; ++x, chunk += std::max<int64_t>(1, chunk / 16)) consider(chunk, 1);
+  const int64_t least = ceil_div(longest, kMaxSlots / 2);
+  for (int pair = 0; pair <= (pairs ? 1 : 0); ++pair) {
+    const int64_t units = pair ? std::max(1, cluster_room(2, sms) / 2) : sms;       // that take an item each
+    const int64_t groups = shared_tiles ? (pair ? (shared_groups + 1) / 2 : shared_groups) : T * (pair ? 1 : own_groups);
+    const int64_t tiles = pair ? (shared_groups + 1) / 2 * shared_tiles + (fp8 ? 0 : T * own_tiles)
+                               : shared_groups * shared_tiles + T * own_groups * own_tiles;
+    for (int rounds = 1; rounds <= 4; ++rounds) {
+      const int64_t pieces = int64_t(rounds) * units / groups;      // of each group of rows
+      if (pieces > 1) consider(std::max(ceil_div(longest, pieces), least), 1, pair);
+      // rounding up to whole chunks can need a few items too many: larger chunks need fewer
+      int64_t chunk = std::max(ceil_div(tiles, int64_t(rounds) * units), least);
+      for (int x = 0; x < 4 && chunk < longest; ++x, chunk += std::max<int64_t>(1, chunk / 16)) consider(chunk, 1, pair);
+    }
   }
   return best;
 }
@@ -962,14 +1474,13 @@ AttnPlan plan_attention(int64_t T, int32_t H, int64_t shared_keys, int64_t own_k
     AttnPlan plan{};
   };
   thread_local Last last;
-  const int32_t wide = fp8 && shared_keys > 0;           // the element type matters to a shared prefix only
-  if (last.T != T || last.H != H || last.shared_keys != shared_keys || last.own_keys != own_keys || last.fp8 != wide || last.sms != sms) {
-    last.plan = make_plan(T, H, shared_keys, own_keys, wide, sms);
+  if (last.T != T || last.H != H || last.shared_keys != shared_keys || last.own_keys != own_keys || last.fp8 != static_cast<int32_t>(fp8) || last.sms != sms) {
+    last.plan = make_plan(T, H, shared_keys, own_keys, fp8, sms);
     last.T = T;
     last.H = H;
     last.shared_keys = shared_keys;
     last.own_keys = own_keys;
-    last.fp8 = wide;
+    last.fp8 = fp8;
     last.sms = sms;
   }
   return last.plan;
@@ -1012,21 +1523,31 @@ cudaError_t launch_attention(const AttnArgs& args, const AttnPlan& p, int* launc
   }
   a.part_o = static_cast<float*>(a.workspace);
   a.part_lse = a.part_o ? a.part_o + size_t(p.slots()) * a.T * a.H * kLatentDim : nullptr;
-  cfg.gridDim = dim3(static_cast<unsigned>(int64_t(p.shared_groups) * p.shared_slots + int64_t(a.T) * p.own_groups * p.own_slots));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  auto kernel = a.kv.fp8 ? attention_kernel<true> : attention_kernel<false>;
   cudaError_t e = set_up(a.kv.fp8);
   if (e != cudaSuccess) return e;
-  if (p.cluster > 1) {
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(p.cluster);
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads);
+  const int64_t shared_items = int64_t(p.shared_groups) * p.shared_slots, own_items = int64_t(a.T) * p.own_groups * p.own_slots;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.pair ? 2 : p.cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  if (p.pair) {
+    const int64_t items = int64_t(p.shared_groups + 1) / 2 * p.shared_slots + (a.kv.fp8 ? 0 : int64_t(a.T) * p.own_slots);
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * items));
+    cfg.dynamicSmemBytes = kPairSmem;
     cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, attention_pair_kernel, a, p);
+    if (e != cudaSuccess) return e;
+    ++*launched;
+    a.first_item = static_cast<int32_t>(shared_items);   // what is left to the single kernel: an FP8 cache's own items
   }
-  e = cudaLaunchKernelEx(&cfg, kernel, a, p);
-  if (e != cudaSuccess) return e;
-  ++*launched;
+  if (!p.pair || (a.kv.fp8 && own_items > 0)) {
+    cfg.gridDim = dim3(static_cast<unsigned>(shared_items + own_items - a.first_item));
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, a.kv.fp8 ? attention_kernel<true> : attention_kernel<false>, a, p);
+    if (e != cudaSuccess) return e;
+    ++*launched;
+  }
   if (p.parts()) {
     cfg.gridDim = dim3(static_cast<unsigned>(int64_t(a.T) * a.H));
     const bool many = p.slots() > 16;

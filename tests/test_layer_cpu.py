@@ -167,7 +167,7 @@ def test_attention_sizes_refused(lib):
                                     None) == 0
     assert lib.dsa_prefix_attention(ctypes.byref(q), ctypes.byref(c), ctypes.byref(t), None, None, 0, 0, 0, 0.1, None, None,
                                     None, 0, None) == 0
-    assert lib.dsa_sparse_attention_workspace_bytes(0, 128, 16) == 0
+    assert lib.dsa_sparse_attention_workspace_bytes(0, 128, 16, _lib.DSA_BF16) == 0
     assert lib.dsa_prefix_attention_workspace_bytes(64, 16, 32768, 33792, _lib.DSA_BF16) > 0    # parts to be joined
     assert lib.dsa_prefix_attention_workspace_bytes(4, 128, 100, 50, _lib.DSA_BF16) == 0
 
