@@ -217,6 +217,7 @@ constexpr int kAttnTile = 64;          // keys per tile; chunks are whole tiles
 struct AttnPlan {
   int32_t shared_groups, shared_slots, shared_chunk;
   int32_t own_groups, own_slots, own_chunk;       // own_groups: row groups of one token
+  int32_t own_rows;                               // rows of an own item
   int32_t cluster;                                // > 1: the own_slots CTAs of a row group are a cluster and join their parts there
   int32_t pair;                                   // pairs of CTAs, each pair against two groups of rows
   int32_t expand;                                 // the shared prefix of an FP8 cache goes to bf16 first

@@ -182,8 +182,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
     item /= p.cluster;
     const int g = item % p.own_groups;
     token = item / p.own_groups;
-    row0 = token * a.H + g * kAttnRows;
-    rows = min(kAttnRows, a.H - g * kAttnRows);
+    row0 = token * a.H + g * p.own_rows;
+    rows = min(p.own_rows, a.H - g * p.own_rows);
   } else if (item < n_shared) {
     row0 = item % p.shared_groups * kAttnRows;
     rows = min(kAttnRows, a.T * a.H - row0);
@@ -193,8 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
     const int g = item % p.own_groups;
     item /= p.own_groups;
     token = item % a.T;
-    row0 = token * a.H + g * kAttnRows;
-    rows = min(kAttnRows, a.H - g * kAttnRows);
+    row0 = token * a.H + g * p.own_rows;
+    rows = min(p.own_rows, a.H - g * p.own_rows);
     slot = p.shared_slots + item / a.T;
   }
   int32_t k0, k1;                // its keys, before lengths are known
@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
 // of 576 values), for the second product half of the values of all its keys (64 rows of 256).  Keys and values have
 // their own stages: a tile's keys are free after its scores, its values after the second product.  CTA 0 issues; CTA 1's
 // two idle warps tell it when their CTA's keys and values have landed.  (64 x 128 heads over 2048 selected keys 69 -> 58
-// us, 512 tokens 805 -> 703.)  A tile takes about 1800 cycles: 1280 of products, about 1500 of shared memory (operands
+// us, 1024 tokens 805 -> 703.)  A tile takes about 1800 cycles: 1280 of products, about 1500 of shared memory (operands
 // 860, copies in 540, weights 100).  Copying the values of a CTA's own keys from its keys' stage, which spares a quarter
 // of the reads of L2, cost 743 us for the 703.
 constexpr uint32_t kPairKeys = (kLatentBlocks + 1) * 4096u;  // 32 rows x 9 blocks
@@ -782,7 +782,8 @@ struct __align__(8) SharedPair {
   uint64_t used[kValueStages];  // the tile's second product is done
   uint64_t taken[2], weights[2];   // CTA 0's: both CTAs have read the scores, have written the weights
   uint64_t listed[kValueStages];
-  uint64_t queries;             // CTA 0's
+  uint64_t queries;             // CTA 0's: both CTAs' queries are in tensor memory
+  uint64_t moved;               // the last stage of values no longer holds queries
   uint64_t drained[2];
   uint32_t tmem;
   int abort;
@@ -844,6 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_pair_kernel(AttnArgs a,
         mbar_init(&sh.drained[i], 1);
       }
       mbar_init(&sh.queries, 2 * kSoftmaxWarps);
+      mbar_init(&sh.moved, kSoftmaxWarps);
       sh.abort = 0;
       sh.key_end = 0;
       fence_barrier_init();
@@ -941,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_pair_kernel(AttnArgs a,
         cp_async16(dk + kLatentBlocks * 4096, static_cast<const __nv_bfloat16*>(kv.rope) + static_cast<int64_t>(max(rk, 0)) * kLatentRope + col * 8, rk >= 0);
       cp_async_arrive(&sh.keys[ks]);
       // values: the rows of the warp's eight keys, this CTA's half of the values
-      ok = mbar_wait<true>(&sh.used[vs], vphase, &sh.abort);
+      ok = mbar_wait<true>(&sh.used[vs], vphase, &sh.abort) && (n != kValueStages + 1 || mbar_wait<true>(&sh.moved, 0, &sh.abort));
       if (!__all_sync(0xffffffffu, ok)) break;
       if (lane == 0) {
         sh.valid[vs][rank][lw] = valid & 15;
@@ -1066,28 +1068,38 @@ __global__ void __launch_bounds__(kThreads, 1) attention_pair_kernel(AttnArgs a,
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     if (tiles > 0) {
-      const int qr = row0 + (r < rows ? r : 0);
-      const int t = rows > 0 ? qr / a.H : 0, h = rows > 0 ? qr - t * a.H : 0;
-      const uint4* ql = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q_latent) + t * a.ql_t + h * a.ql_h);
+      // the queries' values 0 .. 383 pass through the weights' place and the last stage of values: read there by lines,
+      // they are read back by rows
+      auto block = [&](int c) { return smem + (c < 2 ? kPairP + c * kBlock : kPairV + kPairValues * (kValueStages - 1) + (c - 2) * kBlock); };
+      const int col = lane & 7;
 #pragma unroll 1
-      for (int c = 0; c < 192; c += 64) {
-        uint4 x[16];
+      for (int y = warp * 16 + (lane >> 3); y < warp * 16 + 16; y += 4) {
+        const int qr = row0 + (y < rows ? y : 0);
+        const int t = rows > 0 ? qr / a.H : 0, h = rows > 0 ? qr - t * a.H : 0;
+        const __nv_bfloat16* ql = static_cast<const __nv_bfloat16*>(a.q_latent) + t * a.ql_t + h * a.ql_h + col * 8;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = r < rows ? __ldg(ql + c / 4 + e) : make_uint4(0u, 0u, 0u, 0u);
+        for (int c = 0; c < 6; ++c) cp_async16(block(c) + y * 128 + ((col ^ (y & 7)) << 4), ql + c * 64, y < rows);
+      }
+      cp_async_wait_all();
+      named_barrier(3, kSoftmaxWarps * 32);
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          uint32_t v[32];
+      for (int c = 0; c < 6; ++c) {
+        uint32_t v[32];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            v[4 * e] = x[8 * y + e].x; v[4 * e + 1] = x[8 * y + e].y; v[4 * e + 2] = x[8 * y + e].z; v[4 * e + 3] = x[8 * y + e].w;
-          }
-          tmem_st_32x32b_x32(quadrant + kPairTmemQ + c + 32 * y, v);
+        for (int e = 0; e < 8; ++e) {
+          const uint4 x = ld_shared16(block(c) + r * 128 + ((e ^ (r & 7)) << 4));
+          v[4 * e] = x.x; v[4 * e + 1] = x.y; v[4 * e + 2] = x.z; v[4 * e + 3] = x.w;
         }
+        tmem_st_32x32b_x32(quadrant + kPairTmemQ + 32 * c, v);
       }
       tmem_st_wait();
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(&sh.queries, 0);
+      fence_proxy_async_smem();
+      named_barrier(3, kSoftmaxWarps * 32);                // the weights may take their place
+      if (lane == 0) {
+        mbar_arrive(&sh.moved);
+        mbar_arrive_cluster(&sh.queries, 0);
+      }
     }
     int st = 0;
     uint32_t phase = 0;
@@ -1391,10 +1403,14 @@ double finish(int64_t n1, double c1, int64_t n2, double c2, int64_t sms) {
   return hi;
 }
 
-// Cuts a call into items, in units of a tile's time.  An item costs its tiles and about four tiles' time beside them
-// (set-up, queries, result).  Splitting a row costs its join: in a cluster (two to sixteen parts) about two more, through
-// memory with a second kernel about five and the parts' traffic.  A token's rows are whole groups where H is a
-// multiple of 64; sharing a prefix then saves no tile, and shared positions are read by the tokens' own items.
+// Cuts a call into items, in units of a tile's time (1.3 us).  An item costs its tiles and about four tiles' time beside
+// them (set-up, queries, result); its products always have 64 rows, but with fewer rows of its own there is less to
+// write and to join: few tokens are cut into groups of 16 or 32 heads, as long as there are SMs for them (1 x 128 heads
+// over 2048 keys 18.2 -> 14.1 us, 8 x 64 heads over 512 keys 14.3 -> 11.9).  Splitting a row costs its join: in a cluster
+// (two to sixteen parts) one to five tiles' time, through memory a second kernel, which costs the host about 4 us more,
+// and the parts' traffic.  A pair's tile takes 0.85 of the time of one CTA's, an FP8 tile that is expanded on the way 1.4.
+// A token's rows are whole groups where H is a multiple of 64; sharing a prefix then saves no tile, and shared positions
+// are read by the tokens' own items.
 namespace {
 
 AttnPlan make_plan(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, bool fp8, int sms) {
@@ -1412,8 +1428,10 @@ AttnPlan make_plan(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, 
   const int64_t longest = std::max(shared_tiles, own_tiles);
   AttnPlan best{};
   double best_cost = 0.0;
-  auto consider = [&](int64_t chunk, int cluster, bool pair = false) {
+  auto consider = [&](int64_t chunk, int cluster, bool pair = false, int rows = kAttnRows) {
     AttnPlan p{};
+    const int64_t own_groups = ceil_div(H, rows);
+    p.own_rows = rows;
     p.pair = pair;
     p.shared_groups = static_cast<int32_t>(shared_groups);
     p.own_groups = static_cast<int32_t>(own_groups);
@@ -1424,17 +1442,23 @@ AttnPlan make_plan(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, 
     p.expand = expand;
     const int room = cluster > 1 ? cluster_room(cluster, sms) : sms;
     if (p.slots() > kMaxSlots || room < cluster) return;
-    const double join = cluster > 1 ? 2.0 : p.slots() > 1 ? 5.0 + double(p.slots()) * R * 0.0004 : 0.0;
-    double cost = join;
+    // an item's time beside its tiles: for full groups, and for a token's own with the cluster's join
+    const double share = double(rows) / kAttnRows, own_share = std::min(1.0, double(std::min(rows, H)) / kAttnRows);
+    const double full = 4.3, own_tile = fp8 ? 1.4 : 1.0;
+    const double item = 2.8 + 1.5 * own_share + (cluster > 1 ? 0.5 + (1.0 + 0.24 * cluster) * share : 0.0);
+    double cost = cluster == 1 && p.slots() > 1 ? 1.5 + p.slots() * (0.07 + R * 0.0004) : 0.0;
     if (pair) {
       // two SMs an item; an FP8 cache's own items stay with the single kernel, launched behind
-      const double tile = 0.68;
+      const double tile = 0.85, own_item = 3.0 + std::min(2.0, H / 64.0);
       const int64_t shared_pairs = (shared_groups + 1) / 2 * p.shared_slots, own_pairs = fp8 ? 0 : T * p.own_slots;
-      cost += finish(shared_pairs, double(chunk) * tile + 4.5, own_pairs, double(std::min(chunk, own_tiles)) * tile + 4.5, cluster_room(2, sms) / 2);
-      if (fp8 && p.own_slots) cost += 1.0 + finish(T * own_groups * p.own_slots, double(std::min(chunk, own_tiles)) + 4.0, 0, 1.0, sms);
-    } else
-      cost += finish(shared_groups * p.shared_slots, double(chunk) + 4.0, T * own_groups * p.own_slots,
-                                      double(std::min(chunk, own_tiles)) + 4.0, room);
+      cost += finish(shared_pairs, double(chunk) * tile + 5.0, own_pairs, double(std::min(chunk, own_tiles)) * tile + own_item,
+                     cluster_room(2, sms) / 2);
+      if (fp8 && p.own_slots)
+        cost += 1.0 + finish(T * own_groups * p.own_slots, double(std::min(chunk, own_tiles)) * own_tile + item, 0, 1.0, sms);
+    } else {
+      cost += finish(shared_groups * p.shared_slots, double(chunk) * (expand ? 1.0 : own_tile) + full, T * own_groups * p.own_slots,
+                     double(std::min(chunk, own_tiles)) * own_tile + item, room);
+    }
     if (best.slots() == 0 || cost < best_cost) {
       best = p;
       best_cost = cost;
@@ -1444,23 +1468,33 @@ AttnPlan make_plan(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, 
   // in pairs: bf16 keys that at least two groups of rows share
   const bool pairs = (fp8 ? expand : shared_tiles > 0 || own_groups == 2) && cluster_room(2, sms) >= 2;
   if (pairs) consider(longest, 1, true);
-  if (shared_tiles == 0)
-    for (int cluster = 2; cluster <= kMaxCluster && cluster <= own_tiles; cluster *= 2) consider(ceil_div(own_tiles, cluster), cluster);
   // chunks with which the longer part fills one to four rounds of the SMs, alone or with the other part beside it
   const int64_t least = ceil_div(longest, kMaxSlots / 2);
-  for (int pair = 0; pair <= (pairs ? 1 : 0); ++pair) {
+  auto cuts = [&](bool pair, int rows) {
+    const int64_t own = pair ? 1 : ceil_div(H, rows), shared = pair ? (shared_groups + 1) / 2 : shared_groups;
     const int64_t units = pair ? std::max(1, cluster_room(2, sms) / 2) : sms;       // that take an item each
-    const int64_t groups = shared_tiles ? (pair ? (shared_groups + 1) / 2 : shared_groups) : T * (pair ? 1 : own_groups);
-    const int64_t tiles = pair ? (shared_groups + 1) / 2 * shared_tiles + (fp8 ? 0 : T * own_tiles)
-                               : shared_groups * shared_tiles + T * own_groups * own_tiles;
+    const int64_t groups = shared_tiles ? shared : T * own;
+    const int64_t tiles = shared * shared_tiles + (pair && fp8 ? 0 : T * own * own_tiles);
     for (int rounds = 1; rounds <= 4; ++rounds) {
       const int64_t pieces = int64_t(rounds) * units / groups;      // of each group of rows
-      if (pieces > 1) consider(std::max(ceil_div(longest, pieces), least), 1, pair);
+      if (pieces > 1) consider(std::max(ceil_div(longest, pieces), least), 1, pair, rows);
       // rounding up to whole chunks can need a few items too many: larger chunks need fewer
       int64_t chunk = std::max(ceil_div(tiles, int64_t(rounds) * units), least);
-      for (int x = 0; x < 4 && chunk < longest; ++x, chunk += std::max<int64_t>(1, chunk / 16)) consider(chunk, 1, pair);
+      for (int x = 0; x < 4 && chunk < longest; ++x, chunk += std::max<int64_t>(1, chunk / 16)) consider(chunk, 1, pair, rows);
     }
-  }
+  };
+  cuts(false, kAttnRows);
+  if (pairs) cuts(true, kAttnRows);
+  if (shared_tiles == 0)
+    for (int rows = kAttnRows; rows >= 16; rows /= 2) {
+      if (rows < kAttnRows && (rows >= H || T * ceil_div(H, rows) > sms)) continue;
+      for (int cluster = 2; cluster <= kMaxCluster && cluster <= own_tiles; cluster *= 2)
+        consider(ceil_div(own_tiles, cluster), cluster, false, rows);
+      if (rows < kAttnRows) {
+        consider(longest, 1, false, rows);
+        cuts(false, rows);
+      }
+    }
   return best;
 }
 
