@@ -691,3 +691,87 @@ def test_selection_of_everything_is_dense_attention():
     b = api.dsa_prefix_attention(ql, qr, cache, table, seq, lens, SM, max_keys=n)
     assert torch.allclose(a[0].float(), b[0].float(), rtol=2.0 ** -6, atol=2.0 ** -7)
     assert torch.allclose(a[1], b[1], rtol=0, atol=2.0 ** -12)
+
+
+# ------------------------------------------------------------------------------------------------ many rows
+# Sizes at which two CTAs share a tile's keys; the tests above reach one CTA, clusters and groups of 16 heads.
+
+
+@pytest.mark.parametrize("T,H,k,page,fp8,d_r,length,mult", [
+    (50, 128, 512, 64, False, 64, 900, 1), (60, 65, 200, 16, False, 64, 500, 1), (60, 96, 130, 64, False, 0, 300, 30),
+    (40, 128, 640, 1, False, 64, 700, 1), (75, 100, 300, 48, False, 64, 400, 1),
+])
+def test_sparse_attention_of_many_rows(T, H, k, page, fp8, d_r, length, mult):
+    test_sparse_attention(T, H, k, page, fp8, d_r, length, mult)
+
+
+@pytest.mark.parametrize("T,H,prefix,own,page,fp8,d_r", [
+    (70, 24, 6000, 64, 64, False, 64), (16, 24, 9000, 100, 48, False, 64), (9, 128, 3000, 0, 64, False, 0),
+    (23, 128, 3000, 100, 64, True, 64), (40, 128, 500, 1, 16, False, 64),
+])
+def test_prefix_attention_of_many_rows(T, H, prefix, own, page, fp8, d_r):
+    test_prefix_attention(T, H, prefix, own, page, fp8, d_r)
+
+
+def test_many_rows_of_rising_scores():
+    # as above, and a token without a key between the others
+    n, T, H = 640, 44, 128
+    cache, _ = make_cache(n, 64, False, 3)
+    cache.latent.zero_()
+    cache.rope.zero_()
+    cache.latent[:, 0] = torch.arange(n).bfloat16().cuda() / 4
+    cache.latent[:, 300] = (torch.arange(n) % 5).bfloat16().cuda()
+    vals = np.concatenate([f64(cache.latent), f64(cache.rope)], 1)
+    ql, qr = torch.zeros(T, H, 512).bfloat16(), torch.zeros(T, H, 64).bfloat16()
+    ql[:, :, 0] = (torch.arange(H) + 1) / 8                    # up to 16 * 160 = 2560 in the exponent
+    idx = torch.stack([torch.arange(n) if t % 2 else torch.arange(n).flip(0) for t in range(T)]).to(torch.int32)
+    idx[2] = -1
+    table = torch.arange(10, dtype=torch.int32).view(1, 10)
+    out, lse = api.dsa_sparse_attention(ql.cuda(), qr.cuda(), cache, table.cuda(), torch.zeros(T, dtype=torch.int32).cuda(),
+                                        idx.cuda(), 1.0)
+    q = f64(torch.cat([ql, qr], 2))
+    for t in (0, 1, 2, T - 1):
+        check_token(f64(out)[t], f64(lse)[t], q[t], vals[[p for p in idx[t].tolist() if p >= 0]], 1.0, t)
+
+
+def test_many_rows_with_anything_in_masked_places():
+    cache, vals = make_cache(512, 64, False, 1)
+    bad = np.arange(256, 512)
+    cache.latent[bad[:128]] = float("nan")
+    cache.latent[bad[128:]] = float("inf")
+    cache.rope[bad] = float("nan")
+    T, H = 48, 128
+    table = torch.arange(8, dtype=torch.int32).view(1, 8)
+    idx = np.full((T, 330), -1, np.int32)
+    idx[0, 200] = 5
+    idx[1, ::7] = np.arange(48)
+    idx[3:, :40] = np.arange(40)
+    idx[T - 1, :6] = [9, 9, 9, 200, 200, 3]
+    seq = torch.zeros(T, dtype=torch.int32)
+    seq[5] = -1
+    ql, qr = queries(T, H, 2)
+    args = (ql.cuda(), qr.cuda(), cache, table.cuda(), seq.cuda(), torch.from_numpy(idx).cuda(), SM)
+    out, lse = api.dsa_sparse_attention(*args)
+    q = f64(torch.cat([ql, qr], 2))
+    for t in (0, 1, 2, 3, 5, T - 1):
+        keys = [p for p in idx[t] if p >= 0] if seq[t] >= 0 else []
+        check_token(f64(out)[t], f64(lse)[t], q[t], vals[keys], SM, t)
+    # rows that a page table does not hold are left out and reported; the queries' strides; a captured call
+    lens = torch.full((T,), 200, dtype=torch.int32).cuda()
+    holes = table.clone()
+    holes[0, 1] = -1
+    o, l = api.dsa_prefix_attention(args[0], args[1], cache, holes.cuda(), args[4], lens, SM, prefix_len=130, max_keys=500)
+    with pytest.raises(_lib.DsaError):
+        api.dsa_check_device_errors()
+    keys = [p for p in range(200) if not 64 <= p < 128]
+    check_token(f64(o)[0], f64(l)[0], q[0], vals[keys], SM, "holes")
+    lt = ql.transpose(0, 1).contiguous().cuda().transpose(0, 1)
+    joint = torch.cat([qr, torch.zeros(T, H, 40).bfloat16()], 2).cuda()[:, :, :64]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = api.dsa_sparse_attention(lt, joint, *args[2:])
+    for _ in range(2):
+        got[0].fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, got[0]) and torch.equal(lse, got[1])
