@@ -368,6 +368,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
           const uint32_t stage = smem + kOffK + st * kStage + lw * 8 * 128;
           cp_async_wait<1>();                            // all but the latest tile's codes
           __syncwarp();
+          uint4 u[2][4];                                 // together: what follows waits for each of them
+          float s[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r8 = 2 * j + pair;
+            s[j] = __shfl_sync(0xffffffffu, scale2, r8);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) u[h][j] = ld_shared16(codes + r8 * 512 + (((h * 16 + vec) ^ (pair << 2)) << 4));
+          }
           bool ok = true;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -384,15 +393,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int r8 = 2 * j + pair;
-              const float s = __shfl_sync(0xffffffffu, scale2, r8);
-              const uint4 u = ld_shared16(codes + r8 * 512 + (((h * 16 + vec) ^ (pair << 2)) << 4));
-              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+              const uint32_t w[4] = {u[h][j].x, u[h][j].y, u[h][j].z, u[h][j].w};
               const uint32_t base = stage + (h * kHalf + (vec >> 2)) * kBlock + r8 * 128;
 #pragma unroll
               for (int x = 0; x < 2; ++x)
                 st_shared16(base + ((((vec & 3) * 2 + x) ^ r8) << 4),
-                            make_uint4(e4m3x2_to_bf16x2(w[2 * x] & 0xFFFFu, s), e4m3x2_to_bf16x2(w[2 * x] >> 16, s),
-                                       e4m3x2_to_bf16x2(w[2 * x + 1] & 0xFFFFu, s), e4m3x2_to_bf16x2(w[2 * x + 1] >> 16, s)));
+                            make_uint4(e4m3x2_to_bf16x2(w[2 * x] & 0xFFFFu, s[j]), e4m3x2_to_bf16x2(w[2 * x] >> 16, s[j]),
+                                       e4m3x2_to_bf16x2(w[2 * x + 1] & 0xFFFFu, s[j]), e4m3x2_to_bf16x2(w[2 * x + 1] >> 16, s[j])));
             }
             fence_proxy_async_smem();
             __syncwarp();
