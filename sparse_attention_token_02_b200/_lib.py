@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # DSA_INDEXER_LIB may name another build of the same library (e.g. a tuning variant)
@@ -173,6 +174,11 @@ def load() -> ctypes.CDLL:
     lib.dsa_get_last_error.restype = ctypes.c_char_p
     lib.dsa_version.argtypes = []
     lib.dsa_version.restype = ctypes.c_char_p
+    calls = sys.modules.get(__package__ + "._layer_calls")
+    if calls is not None:
+        calls.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+            lib.dsa_rmsnorm_fp8, lib.dsa_latent_append_rope, lib.dsa_sparse_attention,
+            lib.dsa_sparse_attention_workspace_bytes, lib.dsa_prefix_attention, lib.dsa_prefix_attention_workspace_bytes)))
     _lib = lib
     return lib
 

@@ -6,7 +6,8 @@ Compiles every ``csrc/*.cu`` to an object with
 ``-gencode arch=compute_100a,code=sm_100a -lineinfo -O3`` and links them into
 ``libdsa_indexer.so`` next to this file (static CUDA runtime, so loading the
 library needs only the driver; only the ``dsa_*`` C symbols are exported).
-Objects are rebuilt when a source or header is newer.
+``csrc/layer_calls.cpp`` becomes ``_layer_calls.so``, the torch side of the layer's
+calls (g++, torch's headers).  Objects are rebuilt when a source or header is newer.
 """
 
 from __future__ import annotations
@@ -14,10 +15,12 @@ from __future__ import annotations
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +28,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdsa_indexer.so")
+CALLS = os.path.join(PKG, "_layer_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -50,6 +54,15 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _calls_command(src: str) -> list[str]:
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    dirs = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include/torch/csrc/api/include"),
+            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", *(f"-I{d}" for d in dirs), src, "-o", CALLS,
+            "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
 def build(jobs: int = 8, verbose: bool = False, extra: list[str] | None = None, out_dir: str | None = None) -> str:
     """Build the library; `extra` nvcc flags and `out_dir` (objects and .so) serve tuning builds."""
     build_dir = os.path.join(out_dir, "_build") if out_dir else BUILD
@@ -70,12 +83,14 @@ def build(jobs: int = 8, verbose: bool = False, extra: list[str] | None = None, 
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{cmd[0]} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         if verbose and (r.stdout or r.stderr):
             print(r.stdout, r.stderr, flush=True)
 
+    calls = os.path.join(CSRC, "layer_calls.cpp")
+    shared = [_calls_command(calls)] if not out_dir and _stale(CALLS, [calls] + headers) else []
     with cf.ThreadPoolExecutor(max_workers=max(1, jobs)) as ex:
-        list(ex.map(run, cmds))
+        list(ex.map(run, shared + cmds))
     if cmds or _stale(lib_path, objs):
         run([nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", lib_path, *objs])
     return lib_path

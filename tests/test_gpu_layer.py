@@ -775,3 +775,67 @@ def test_many_rows_with_anything_in_masked_places():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, got[0]) and torch.equal(lse, got[1])
+
+
+def test_compiled_and_python_calls_agree(monkeypatch):
+    # the compiled calls and their Python forms: the same results, given and new outputs, and the same refusals
+    assert api._layer_calls is not None
+    cache, _ = make_cache(512, 64, False, 1)
+    fp8, _ = make_cache(512, 64, True, 2)
+    table = torch.arange(8, dtype=torch.int32).view(1, 8).cuda()
+    T, H = 3, 40
+    ql, qr = (x.cuda() for x in queries(T, H, 2))
+    seq = torch.tensor([0, -1, 0], dtype=torch.int32).cuda()
+    idx = torch.stack([torch.randperm(512, generator=gen(t))[:200] for t in range(T)]).to(torch.int32).cuda()
+    lens = torch.tensor([300, 5, 512], dtype=torch.int32).cuda()
+    x, w = torch.randn(5, 320, generator=gen(3)).cuda(), torch.randn(256, generator=gen(4)).bfloat16().cuda()
+    pos = torch.tensor([1, 70, 200], dtype=torch.int32).cuda()
+    new = torch.randn(3, 700, generator=gen(5)).cuda()
+
+    def calls():
+        res = torch.ones(5, 256).cuda()
+        given = torch.empty(5, 256, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(5, device="cuda")
+        got = [*api.dsa_rmsnorm_fp8(x[:, :256], w, 1e-5, residual=res), *api.dsa_rmsnorm_fp8(x[:, 64:], w, group=0)[:2]]
+        codes, scale, out = api.dsa_rmsnorm_fp8(x[:, :256], w, residual=res, residual_out=res, group=0, codes=given[0], scale=given[1],
+                                                normed=torch.empty(5, 256, dtype=torch.bfloat16, device="cuda"))
+        assert codes is given[0] and scale is given[1] and out is res
+        got += [codes.view(torch.uint8), scale, out.clone()]
+        for c in (cache, fp8):
+            for kw in (dict(rope_dim=32, interleaved=False), dict(base=500.0)):
+                api.dsa_latent_append_rope(c, table, new[:, 4:516], new[:, 600:664], seq, pos, **kw)
+            got += [c.latent.clone(), c.rope.clone()]
+            got += api.dsa_sparse_attention(ql, qr, c, table, seq, idx, SM)
+            got += api.dsa_prefix_attention(ql, qr, c, table, seq, lens, SM)
+            out, lse = torch.empty(T, H, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(T, H, device="cuda")
+            ws = torch.empty(api.dsa_prefix_attention_workspace_bytes(T, H, 64, 512, c.fp8), dtype=torch.uint8, device="cuda")
+            r = api.dsa_prefix_attention(ql, qr, c, table, seq, lens, SM, 64, 0, 512, out=out, lse=lse, workspace=ws)
+            assert r[0] is out and r[1] is lse
+            got += r
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        got += api.dsa_sparse_attention(ql, qr, cache, table, seq, idx, SM, stream=side)
+        side.synchronize()
+        return got
+
+    def refusals():
+        small = torch.empty(16, dtype=torch.uint8, device="cuda")
+        for f, kind in (
+            (lambda: api.dsa_rmsnorm_fp8(x[:, :200].half(), w[:200]), TypeError),
+            (lambda: api.dsa_rmsnorm_fp8(x[:, :200], w[:200]), _lib.DsaError),                   # d % 16
+            (lambda: api.dsa_rmsnorm_fp8(x[:, :256], w, residual=torch.ones(5, 255).cuda()), ValueError),
+            (lambda: api.dsa_sparse_attention(ql, qr, cache, table, seq, idx.long(), SM), TypeError),
+            (lambda: api.dsa_sparse_attention(ql, qr[:, :, ::2], cache, table, seq, idx, SM), ValueError),
+            (lambda: api.dsa_sparse_attention(ql, qr, cache, table, seq, idx.cpu(), SM), ValueError),
+            (lambda: api.dsa_sparse_attention(ql, qr, cache, table, seq, idx, float("nan")), _lib.DsaError),
+            (lambda: api.dsa_prefix_attention(ql, qr, fp8, table, seq, lens, SM, 400, 0, 512, workspace=small), _lib.DsaError),
+            (lambda: api.dsa_latent_append_rope(cache, table, new[:, :512], new[:, 600:664], seq[:2], pos), ValueError),
+        ):
+            with pytest.raises(kind):
+                f()
+
+    a = calls()
+    refusals()
+    monkeypatch.setattr(api, "_layer_calls", None)
+    b = calls()
+    refusals()
+    assert len(a) == len(b) and all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in zip(a, b))

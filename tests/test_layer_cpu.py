@@ -195,3 +195,20 @@ def test_binding_refusals():
         api.dsa_rmsnorm_fp8(torch.zeros(16, 32).t(), torch.zeros(16))
     with pytest.raises(ValueError, match="group"):
         api.dsa_rmsnorm_fp8(torch.zeros(16, 32), torch.zeros(32), group=64)
+
+
+def test_compiled_calls_answer_only_plain_ones():
+    # built with the library; a call that it does not make itself is left to the Python form, without an error of its own
+    calls = api._layer_calls
+    assert calls is not None
+    _lib.load()
+    x = torch.zeros(2, 128)
+    assert calls.rmsnorm(x, x[0], 1e-6, None, 128, None, None, None, None) is None
+    assert calls.rmsnorm(None, 3, "eps", x, [], None, None, None, None) is None
+    assert calls.rmsnorm() is None and calls.append(1) is None and calls.sparse(x) is None and calls.prefix() is None
+    idx = torch.zeros(2, 1, dtype=torch.int32)
+    ids = torch.zeros(2, dtype=torch.int32)
+    q = torch.zeros(2, 16, 512, dtype=torch.bfloat16)
+    assert calls.sparse(q, q[:, :, :64], x, None, None, 64, idx, ids, idx, 1.0, None, None, None) is None
+    with pytest.raises(TypeError):
+        calls.bind(1, 2)
