@@ -1291,7 +1291,8 @@ __global__ void __launch_bounds__(256) expand_kernel(LatentView kv, int32_t seq,
 
 // Joins the parts of one row: weights 2^(lse_i - max) over their sum, made by a lane per part; then 128 threads add up
 // four values each, eight parts' loads at a time.  Bound by the latency of those loads: rows of many parts get four such
-// groups of threads (128 rows of 74 parts took 14 us with one).
+// groups of threads (128 rows of 74 parts took 14 us with one; attention of 256 rows in 16 parts 16.3 -> 13.9 us, but
+// of 1024 rows in 10 parts 102 -> 107).
 template <int GROUPS>
 __global__ void __launch_bounds__(GROUPS * 128) attention_join_kernel(AttnArgs a, int slots) {
   __shared__ float weight[kMaxSlots];
@@ -1413,11 +1414,10 @@ double finish(int64_t n1, double c1, int64_t n2, double c2, int64_t sms) {
 // Cuts a call into items, in units of a tile's time (1.3 us).  An item costs its tiles and about four tiles' time beside
 // them (set-up, queries, result); its products always have 64 rows, but with fewer rows of its own there is less to
 // write and to join: few tokens are cut into groups of 16 or 32 heads, as long as there are SMs for them (1 x 128 heads
-// over 2048 keys 18.2 -> 14.1 us, 8 x 64 heads over 512 keys 14.3 -> 11.9).  Splitting a row costs its join: in a cluster
-// (two to sixteen parts) one to five tiles' time, through memory a second kernel, which costs the host about 4 us more,
-// and the parts' traffic.  A pair's tile takes 0.85 of the time of one CTA's, an FP8 tile that is expanded on the way 1.4.
-// A token's rows are whole groups where H is a multiple of 64; sharing a prefix then saves no tile, and shared positions
-// are read by the tokens' own items.
+// over 2048 keys 15.5 -> 12.6 us, 8 x 64 heads over 512 keys 14.3 -> 11.9).  Splitting a row costs its join: in a cluster
+// (two to sixteen parts) one to five tiles' time, through memory a second kernel and the parts' traffic.  A pair's tile
+// takes 0.85 of the time of one CTA's, an FP8 tile that is expanded on the way 1.4.  A token's rows are whole groups where
+// H is a multiple of 64; sharing a prefix then saves no tile, and shared positions are read by the tokens' own items.
 namespace {
 
 AttnPlan make_plan(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, bool fp8, int sms) {
@@ -1453,7 +1453,7 @@ AttnPlan make_plan(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, 
     const double share = double(rows) / kAttnRows, own_share = std::min(1.0, double(std::min(rows, H)) / kAttnRows);
     const double full = 4.3, own_tile = fp8 ? 1.4 : 1.0;
     const double item = 2.8 + 1.5 * own_share + (cluster > 1 ? 0.5 + (1.0 + 0.24 * cluster) * share : 0.0);
-    double cost = cluster == 1 && p.slots() > 1 ? 1.5 + p.slots() * (0.07 + R * 0.0004) : 0.0;
+    double cost = cluster == 1 && p.slots() > 1 ? 0.5 + p.slots() * (0.07 + R * 0.0004) : 0.0;
     if (pair) {
       // two SMs an item; an FP8 cache's own items stay with the single kernel, launched behind
       const double tile = 0.85, own_item = 3.0 + std::min(2.0, H / 64.0);
@@ -1590,8 +1590,9 @@ cudaError_t launch_attention(const AttnArgs& args, const AttnPlan& p, int* launc
     ++*launched;
   }
   if (p.parts()) {
-    cfg.gridDim = dim3(static_cast<unsigned>(int64_t(a.T) * a.H));
-    const bool many = p.slots() > 16;
+    const int64_t R = int64_t(a.T) * a.H;
+    cfg.gridDim = dim3(static_cast<unsigned>(R));
+    const bool many = p.slots() > (R <= 512 ? 8 : 16);   // few rows leave room for the larger blocks
     cfg.blockDim = dim3(many ? 512 : 128);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
