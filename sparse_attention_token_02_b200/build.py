@@ -60,7 +60,7 @@ def _calls_command(src: str) -> list[str]:
     dirs = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include/torch/csrc/api/include"),
             os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", *(f"-I{d}" for d in dirs), src, "-o", CALLS,
-            "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+            "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
 
 
 def build(jobs: int = 8, verbose: bool = False, extra: list[str] | None = None, out_dir: str | None = None) -> str:

@@ -5,7 +5,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/ops/empty_cuda_dispatch.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -82,7 +82,7 @@ struct Result {
   void* ptr = nullptr;
   Result(const Call& call, PyObject* o, at::IntArrayRef sizes, at::TensorOptions options) {
     if (o == Py_None) {
-      made = at::empty(sizes, options);
+      made = at::cuda::empty(sizes, options);
       ptr = made.data_ptr();
       return;
     }
@@ -224,7 +224,7 @@ struct Outputs {
       workspace = given->data_ptr();
       bytes = static_cast<size_t>(given->numel() * given->element_size());
     } else if (need) {
-      made = at::empty({static_cast<int64_t>(need)}, like.options().dtype(at::kByte));
+      made = at::cuda::empty({static_cast<int64_t>(need)}, like.options().dtype(at::kByte));
       workspace = made.data_ptr();
       bytes = need;
     }
