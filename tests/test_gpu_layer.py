@@ -839,3 +839,33 @@ def test_compiled_and_python_calls_agree(monkeypatch):
     b = calls()
     refusals()
     assert len(a) == len(b) and all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("rows,d,dtype,residual,group", [
+    (1400, 128, "bf16", True, 128), (900, 2064, "bf16", False, 128), (700, 4112, "f32", True, 128), (650, 4112, "f32", True, 0),
+    (640, 8192, "bf16", True, 128), (620, 8176, "f32", False, 0), (5000, 48, "f32", False, 128), (300, 8208, "bf16", True, 128),
+])
+def test_norm_of_more_rows_than_stay_resident(rows, d, dtype, residual, group):
+    # a block takes several rows, the next one's loads under way: each is what it is alone, in place too
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    g = gen(rows + d)
+    x, w = torch.randn(rows, d, generator=g).to(dt).cuda(), (1 + 0.2 * torch.randn(d, generator=g)).to(dt).cuda()
+    res = (4 * torch.randn(rows, d, generator=g)).to(dt).cuda() if residual else None
+    x[rows // 2] = 0
+    if residual:
+        res[rows // 2] = 0
+    x[rows - 2, 3] = float("inf")
+    pick = torch.tensor([0, 1, rows // 2, rows // 2 + 1, rows - 3, rows - 2, rows - 1])
+    alone = api.dsa_rmsnorm_fp8(x[pick].contiguous(), w, 1e-6, residual=res[pick].contiguous() if residual else None, group=group)
+    inplace = res.clone() if residual else None
+    codes, scale, out = api.dsa_rmsnorm_fp8(x, w, 1e-6, residual=inplace, residual_out=inplace, group=group)
+    assert torch.equal(codes[pick], alone[0]) and torch.equal(scale[pick].view(torch.int32), alone[1].view(torch.int32))
+    if residual:
+        assert out is inplace and torch.equal(out[pick], alone[2]) and torch.equal(out, (x.float() + res.float()).to(dt))
+    finite = torch.arange(rows) != rows - 2
+    s, y = L.rmsnorm(f64(x[finite]), f64(w), 1e-6, f64(res[finite]) if residual else None)
+    ref = L.group_scales(y, group)
+    assert np.all(np.abs(f64(scale)[finite] - ref) <= 2.0 ** -18 * ref)
+    wide = np.repeat(f64(scale)[finite], group or d, axis=1)[:, :d]
+    got = e4m3_decode(codes.cpu().numpy()[finite]) * wide
+    assert np.all(np.abs(got - y) <= np.maximum(2.0 ** -4 * np.abs(y), 2.0 ** -10 * wide) + 2.0 ** -17 * np.abs(y))
