@@ -4,16 +4,16 @@
 //     y = s * rsqrt(mean(s^2) + eps) * weight
 //     scale = absmax(y) / 448 per row or per 128 values (1 where all are zero), codes = E4M3(y / scale)
 // Everything between the loads and the stores is fp32: the norm and the codes are taken from the
-// unrounded sum, so the only roundings are the stored residual's, the codes' and (where asked for)
-// the bf16 copy's.  The quotient y / scale is a product with the correctly rounded reciprocal, within
-// one fp32 ulp of it.
+// unrounded sum, so the only roundings to fewer bits are the stored residual's, the codes' and (where asked for)
+// the bf16 copy's.
 //
-// y is inv * (s * weight): the products and the groups' maxima are made before the row's sum is known, and what follows it
-// is one factor inv / scale a group.
+// With t = s * weight, y is inv * t: products and maxima are made before the row's sum is known, y / scale is
+// t * (448 / max|t|), and the sum enters the scale alone.  The reciprocal square root is within two fp32 ulps, 1 / 448 and
+// the quotient's reciprocal within one.
 //
 // Bound by HBM: each input is read and each output written once (7 bytes a value for bf16 with a residual); 16384 x 7168
-// rows back to back in a graph take 129 us (98 % of the measured copy rate), without a residual 89 us (61 %: there the
-// instructions, about 12 a value, weigh as much).  A CTA keeps a row in registers between the sum and the codes and has
+// rows back to back in a graph take 130 us (97 % of the measured copy rate), without a residual 94 us (58 %: there the
+// instructions, some 20 a value, weigh as much).  A CTA keeps a row in registers between the sum and the codes and has
 // its next row's loads under way meanwhile: one CTA a row and weights applied after the sum took 133 and 107 us, and
 // 17 us for 16384 rows of 128 values that take 6 now.  A ring of rows in shared memory (155 us) cost more than it hid.
 #include <cuda_bf16.h>
@@ -28,6 +28,9 @@ namespace dsa {
 namespace {
 
 constexpr int kVec = 8;                       // values per thread and step: 16 bytes of bf16
+constexpr float kTiny = 0x1p-100f, kLift = 0x1p64f;
+// Eight squares above kLarge are summed as those of s * kDown: no row's sum overflows.
+constexpr float kLarge = 0x1p96f, kDown = 0x1p-72f;
 
 // Eight values as they lie in memory
 template <bool F32>
@@ -119,9 +122,9 @@ template <bool F32, int VPT, bool RES>
 __global__ void __launch_bounds__(VPT <= 2 ? 512 : 1024, VPT <= 2 ? 2 : 1) rmsnorm_kernel(NormArgs a) {
   constexpr bool kAhead = VPT <= 2;
   constexpr int kWarps = kAhead ? 16 : 32;
-  __shared__ float4 part[2][2][kWarps / 4];              // two rows in turn: every warp's sum and maximum
+  __shared__ float4 part[2][3][kWarps / 4];              // two rows in turn: every warp's sum, maximum and sum of large squares
   const int nvec = a.d / kVec, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < 4 * kWarps; i += blockDim.x) reinterpret_cast<float*>(part)[i] = 0.f;   // warps that are not there
+  for (int i = tid; i < 6 * kWarps; i += blockDim.x) reinterpret_cast<float*>(part)[i] = 0.f;   // warps that are not there
   __syncthreads();
   grid_dependency_wait();
   launch_dependents();
@@ -137,12 +140,13 @@ __global__ void __launch_bounds__(VPT <= 2 ? 512 : 1024, VPT <= 2 ? 2 : 1) rmsno
       }
     }
   };
+  const float per_value = 1.0f / static_cast<float>(a.d);
   int64_t row = blockIdx.x;
   load(row);
   for (int turn = 0; row < a.rows; row += gridDim.x, turn ^= 1) {
     // t = s * weight: what is left of y is the row's factor, known after the sum
     float t[VPT][kVec], top[VPT];
-    float sq = 0.f;
+    float sq = 0.f, large = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = i * blockDim.x + tid;
@@ -161,9 +165,17 @@ __global__ void __launch_bounds__(VPT <= 2 ? 512 : 1024, VPT <= 2 ? 2 : 1) rmsno
         float w[kVec];
         if (a.w_f32) widen<true>(load8<true>(a.weight, v * kVec), w);
         else widen<false>(load8<false>(a.weight, v * kVec), w);
+        float q = 0.f;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) q += t[i][e] * t[i][e];
+        if (q > kLarge) {
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) large += (t[i][e] * kDown) * (t[i][e] * kDown);
+        } else {
+          sq += q;
+        }
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
-          sq += t[i][e] * t[i][e];
           t[i][e] *= w[e];
           top[i] = fmaxf(top[i], fabsf(t[i][e]));
         }
@@ -183,11 +195,17 @@ __global__ void __launch_bounds__(VPT <= 2 ? 512 : 1024, VPT <= 2 ? 2 : 1) rmsno
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], o));
     }
+    const bool any = __any_sync(0xffffffffu, large != 0.f);
+    if (any) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) large += __shfl_xor_sync(0xffffffffu, large, o);
+    }
     if (lane == 0) {
       reinterpret_cast<float*>(part[turn][0])[warp] = sq;
       reinterpret_cast<float*>(part[turn][1])[warp] = top[0];
+      reinterpret_cast<float*>(part[turn][2])[warp] = large;
     }
-    __syncthreads();
+    const bool wild = __syncthreads_or(any);
     float sum = 0.f, most = 0.f;
 #pragma unroll
     for (int i = 0; i < kWarps / 4; ++i) {
@@ -201,7 +219,29 @@ __global__ void __launch_bounds__(VPT <= 2 ? 512 : 1024, VPT <= 2 ? 2 : 1) rmsno
         most = fmaxf(fmaxf(most, fmaxf(p.x, p.y)), fmaxf(p.z, p.w));
       }
     }
-    const float inv = 1.0f / sqrtf(sum / static_cast<float>(a.d) + a.eps);
+    float inv = rsqrtf(sum * per_value + a.eps);
+    if (wild) {
+      float down = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps / 4; ++i) {
+        const float4 p = part[turn][2][i];
+        down += (p.x + p.y) + (p.z + p.w);
+      }
+      inv = rsqrtf((down + sum * (kDown * kDown)) * per_value + a.eps * (kDown * kDown)) * kDown;
+    }
+    const int64_t at = row * a.d;
+    if (a.normed) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = i * blockDim.x + tid;
+        if (v < nvec) {
+          float y[kVec];
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) y[e] = t[i][e] * inv;
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.normed) + at + v * kVec) = bf16x8(y);
+        }
+      }
+    }
     // A group's scale is worked out once for the thread's VPT groups: by every VPT-th part of its 16 lanes.
     constexpr int kShift = VPT == 4 ? 2 : VPT == 2 ? 3 : 4;
     const int mine = (lane >> kShift) & (VPT - 1);
@@ -212,9 +252,11 @@ __global__ void __launch_bounds__(VPT <= 2 ? 512 : 1024, VPT <= 2 ? 2 : 1) rmsno
       for (int i = 1; i < VPT; ++i)
         if (mine == i) amax = top[i];
     }
-    amax *= inv;
-    const float sc = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-    const float factor = inv * __frcp_rn(sc);
+    // y / scale = t * 448 / max|t|.  Values so small that the quotient could overflow go up by 2^64 first.
+    const float lift = amax < kTiny ? kLift : 1.0f;
+    const float peak = amax * inv;                         // 0 or NaN: the scale is 1, the codes are those of y
+    const float sc = peak > 0.f ? peak * (1.0f / 448.0f) : 1.0f;
+    const float factor = peak > 0.f ? 448.0f * __frcp_rn(amax * lift) : inv;
     if (a.group) {
       const int first = (mine * blockDim.x + tid) & ~15;    // the group's first vector
       if ((lane & ((1 << kShift) - 1)) == 0 && first < nvec) a.scale[row * ((a.d + 127) / 128) + first / 16] = sc;
@@ -224,17 +266,17 @@ __global__ void __launch_bounds__(VPT <= 2 ? 512 : 1024, VPT <= 2 ? 2 : 1) rmsno
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = i * blockDim.x + tid;
-      const float k = VPT == 1 || !a.group ? factor : __shfl_sync(0xffffffffu, factor, (lane & 16) | i << kShift);
-      if (v < nvec) {
-        *reinterpret_cast<uint2*>(a.codes + row * a.d + v * kVec) =
+      const int from = (lane & 16) | i << kShift;
+      const float k = VPT == 1 || !a.group ? factor : __shfl_sync(0xffffffffu, factor, from);
+      const float largest = a.group ? top[i] : most;
+      if (largest < kTiny && largest * inv > 0.f) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) t[i][e] *= kLift;
+      }
+      if (v < nvec)
+        *reinterpret_cast<uint2*>(a.codes + at + v * kVec) =
             make_uint2(e4m3x4(t[i][0] * k, t[i][1] * k, t[i][2] * k, t[i][3] * k),
                        e4m3x4(t[i][4] * k, t[i][5] * k, t[i][6] * k, t[i][7] * k));
-        if (a.normed) {
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) t[i][e] *= inv;
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.normed) + row * a.d + v * kVec) = bf16x8(t[i]);
-        }
-      }
     }
     if (!kAhead) break;
   }

@@ -869,3 +869,22 @@ def test_norm_of_more_rows_than_stay_resident(rows, d, dtype, residual, group):
     wide = np.repeat(f64(scale)[finite], group or d, axis=1)[:, :d]
     got = e4m3_decode(codes.cpu().numpy()[finite]) * wide
     assert np.all(np.abs(got - y) <= np.maximum(2.0 ** -4 * np.abs(y), 2.0 ** -10 * wide) + 2.0 ** -17 * np.abs(y))
+
+
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("mag", [2.0 ** -122, 2.0 ** -104, 2.0 ** -98, 2.0 ** 60])
+def test_norm_of_small_and_large_values(mag, group):
+    # the codes keep their precision where 448 / max|t| would overflow, and a group of such values beside ordinary ones.
+    # A sum of squares that underflows to nothing is as far off as eps is large against it: nothing here.
+    x = (torch.rand(3, 384, generator=gen(7)) + 0.5) * torch.sign(torch.randn(3, 384, generator=gen(8)))
+    x[:2] *= mag
+    x[1, 128:256] /= mag if mag < 1 else 1
+    x[2, 256:] = 0
+    w = torch.ones(384)
+    codes, scale, _ = api.dsa_rmsnorm_fp8(x.cuda(), w.cuda(), 1e-6, group=group)
+    s, y = L.rmsnorm(f64(x), f64(w), 1e-6)
+    ref = L.group_scales(y, group)
+    assert np.all(np.abs(f64(scale) - ref) <= 2.0 ** -18 * ref + 2.0 ** -149)      # and half a step of subnormal numbers
+    wide = np.repeat(f64(scale), group or 384, axis=1)
+    got = e4m3_decode(codes.cpu().numpy()) * wide
+    assert np.all(np.abs(got - y) <= np.maximum(2.0 ** -4 * np.abs(y), 2.0 ** -10 * wide) + 2.0 ** -17 * np.abs(y) + 448 * 2.0 ** -149)
