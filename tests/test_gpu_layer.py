@@ -888,3 +888,41 @@ def test_norm_of_small_and_large_values(mag, group):
     wide = np.repeat(f64(scale), group or 384, axis=1)
     got = e4m3_decode(codes.cpu().numpy()) * wide
     assert np.all(np.abs(got - y) <= np.maximum(2.0 ** -4 * np.abs(y), 2.0 ** -10 * wide) + 2.0 ** -17 * np.abs(y) + 448 * 2.0 ** -149)
+
+
+def test_calls_from_two_threads():
+    # the host path gives up the interpreter's lock while the library works: each thread has its own stream
+    import threading
+
+    cache, _ = make_cache(2048, 64, False, 1)
+    table = torch.arange(32, dtype=torch.int32).view(1, 32).cuda()
+    sizes = [(1, 128, 700), (50, 128, 500), (3, 16, 90)]
+    args = []
+    for T, H, k in sizes:
+        ql, qr = (x.cuda() for x in queries(T, H, k))
+        idx = torch.stack([torch.randperm(2048, generator=gen(t))[:k] for t in range(T)]).to(torch.int32).cuda()
+        args.append((ql, qr, cache, table, torch.zeros(T, dtype=torch.int32).cuda(), idx, SM))
+    x, w = torch.randn(400, 1024, generator=gen(2)).cuda(), torch.ones(1024, device="cuda")
+    want = [api.dsa_sparse_attention(*a)[0] for a in args], api.dsa_rmsnorm_fp8(x, w)[0]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(order):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(30):
+                    got = {i: api.dsa_sparse_attention(*args[i])[0] for i in order}
+                    codes = api.dsa_rmsnorm_fp8(x, w)[0]
+                    torch.cuda.current_stream().synchronize()
+                    if not torch.equal(codes, want[1]) or any(not torch.equal(got[i], want[0][i]) for i in order):
+                        bad.append(order)
+        except Exception as e:                               # reported by the main thread
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=(o,)) for o in ([0, 1, 2], [2, 1, 0], [1, 0, 2])]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+    api.dsa_check_device_errors()
