@@ -765,10 +765,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
 // tensor cores' full rate, where 64 rows on one run at half.  For the scores a CTA holds half of a tile's keys (32 rows
 // of 576 values), for the second product half of the values of all its keys (64 rows of 256).  Keys and values have
 // their own stages: a tile's keys are free after its scores, its values after the second product.  CTA 0 issues; CTA 1's
-// two idle warps tell it when their CTA's keys and values have landed.  (64 x 128 heads over 2048 selected keys 69 -> 58
-// us, 1024 tokens 805 -> 703.)  A tile takes about 1800 cycles: 1280 of products, about 1500 of shared memory (operands
+// two idle warps tell it when their CTA's keys and values have landed.  (64 x 128 heads over 2048 selected keys 69 us with
+// one CTA per 64 rows, 56 in pairs; 1024 tokens 805 and 687.)  A tile takes about 1800 cycles: 1280 of products, about 1500 of shared memory (operands
 // 860, copies in 540, weights 100).  Copying the values of a CTA's own keys from its keys' stage, which spares a quarter
-// of the reads of L2, cost 743 us for the 703.
+// of the reads of L2, cost 743 us for the 703 of then; a third stage of keys for one of values changed nothing.
 constexpr uint32_t kPairKeys = (kLatentBlocks + 1) * 4096u;  // 32 rows x 9 blocks
 constexpr uint32_t kPairValues = 4 * kBlock;                 // 64 rows x 4 blocks
 constexpr int kKeyStages = 2, kValueStages = 3;
@@ -1424,7 +1424,8 @@ AttnPlan make_plan(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, 
   const int64_t R = T * H, shared_groups = ceil_div(R, kAttnRows), own_groups = ceil_div(H, kAttnRows);
   int64_t shared_tiles = ceil_div(shared_keys, kAttnTile);
   // Expanding FP8 rows to bf16 costs the loading warps more time than a tile's products take; a prefix that many
-  // groups of rows read is expanded once instead (23 x 128 heads over 16001 keys: 248 -> 173 us).
+  // groups of rows read is expanded once instead (23 x 128 heads over 16001 keys: 248 -> 173 us
+  // then, 147 in pairs).
   const bool expand = fp8 && shared_groups >= 4 && shared_groups * shared_tiles >= 8 * sms;
   if (H % kAttnRows == 0 && !expand) {
     own_keys += shared_keys;
