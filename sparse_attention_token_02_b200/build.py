@@ -54,11 +54,15 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _calls_command(src: str) -> list[str]:
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+def _calls_command(src: str) -> list[str] | None:
+    """None where torch or Python's headers are not there: the package then makes these calls from Python."""
+    spec, python = importlib.util.find_spec("torch"), sysconfig.get_paths()["include"]
+    if spec is None or not os.path.exists(os.path.join(python, "Python.h")):
+        return None
+    torch = spec.submodule_search_locations[0]
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     dirs = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include/torch/csrc/api/include"),
-            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+            os.path.join(cuda, "include"), python]
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", *(f"-I{d}" for d in dirs), src, "-o", CALLS,
             "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
 
@@ -88,7 +92,8 @@ def build(jobs: int = 8, verbose: bool = False, extra: list[str] | None = None, 
             print(r.stdout, r.stderr, flush=True)
 
     calls = os.path.join(CSRC, "layer_calls.cpp")
-    shared = [_calls_command(calls)] if not out_dir and _stale(CALLS, [calls] + headers) else []
+    command = _calls_command(calls) if not out_dir and _stale(CALLS, [calls] + headers) else None
+    shared = [command] if command else []
     with cf.ThreadPoolExecutor(max_workers=max(1, jobs)) as ex:
         list(ex.map(run, shared + cmds))
     if cmds or _stale(lib_path, objs):
