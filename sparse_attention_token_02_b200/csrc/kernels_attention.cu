@@ -1452,9 +1452,12 @@ AttnPlan make_plan(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, 
     if (p.slots() > kMaxSlots || room < cluster) return;
     // an item's time beside its tiles: for full groups, and for a token's own with the cluster's join
     const double share = double(rows) / kAttnRows, own_share = std::min(1.0, double(std::min(rows, H)) / kAttnRows);
-    const double full = 4.3, own_tile = fp8 ? 1.4 : 1.0;
-    const double item = 2.8 + 1.5 * own_share + (cluster > 1 ? 0.5 + (1.0 + 0.24 * cluster) * share : 0.0);
-    double cost = cluster == 1 && p.slots() > 1 ? 0.5 + p.slots() * (0.07 + R * 0.0004) : 0.0;
+    const double full = 4.3, fp8_start = fp8 && chunk > 1 ? 0.8 : 0.0;
+    const double item = 2.8 + 1.5 * own_share + fp8_start + (cluster > 1 ? 1.9 + (1.0 + 0.24 * cluster) * share : 0.0);
+    // bf16 keys of tokens that each read their own: 115 SMs take all that HBM gives
+    const double readers = double(std::min<int64_t>(T * own_groups * p.own_slots, sms)) / own_groups;
+    const double own_tile = fp8 ? 1.4 : std::max(1.0, readers / 115);
+    double cost = cluster == 1 && p.slots() > 1 ? 1.9 + p.slots() * (0.045 + R * 0.0004) : 0.0;
     if (pair) {
       // two SMs an item; an FP8 cache's own items stay with the single kernel, launched behind
       const double tile = 0.85, own_item = 3.0 + std::min(2.0, H / 64.0);
