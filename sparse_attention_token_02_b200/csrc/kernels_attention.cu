@@ -1290,9 +1290,10 @@ __global__ void __launch_bounds__(256) expand_kernel(LatentView kv, int32_t seq,
 }
 
 // Joins the parts of one row: weights 2^(lse_i - max) over their sum, made by a lane per part; then 128 threads add up
-// four values each, eight parts' loads at a time.  Bound by the latency of those loads: rows of many parts get four such
-// groups of threads (128 rows of 74 parts took 14 us with one; attention of 256 rows in 16 parts 16.3 -> 13.9 us, but
-// of 1024 rows in 10 parts 102 -> 107).
+// four values each, eight parts' loads at a time.  Bound by the latency of those loads: rows of many parts get two or
+// four such groups of threads (128 rows of 74 parts took 14 us with one).  Blocks of four find no room beside the first
+// kernel's, those of two do: attention of 384 rows in 11 parts 17.9 us with four and 16.4 with two, of 256 rows in 16
+// parts, few enough blocks, 13.8 and 14.6; of 512 rows in 16 parts 24.6 with one and 22.9 with two.
 template <int GROUPS>
 __global__ void __launch_bounds__(GROUPS * 128) attention_join_kernel(AttnArgs a, int slots) {
   __shared__ float weight[kMaxSlots];
@@ -1596,11 +1597,12 @@ cudaError_t launch_attention(const AttnArgs& args, const AttnPlan& p, int* launc
   if (p.parts()) {
     const int64_t R = int64_t(a.T) * a.H;
     cfg.gridDim = dim3(static_cast<unsigned>(R));
-    const bool many = p.slots() > (R <= 512 ? 8 : 16);   // few rows leave room for the larger blocks
-    cfg.blockDim = dim3(many ? 512 : 128);
+    const int join = p.slots() > (R <= 256 ? 8 : 16) ? 4 : p.slots() > 8 ? 2 : 1;      // groups of threads
+    cfg.blockDim = dim3(128 * join);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, many ? attention_join_kernel<4> : attention_join_kernel<1>, a, static_cast<int>(p.slots()));
+    e = cudaLaunchKernelEx(&cfg, join == 4 ? attention_join_kernel<4> : join == 2 ? attention_join_kernel<2> : attention_join_kernel<1>, a,
+                           static_cast<int>(p.slots()));
     if (e != cudaSuccess) return e;
     ++*launched;
   }
