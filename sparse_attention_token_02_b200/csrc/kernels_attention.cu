@@ -1597,7 +1597,7 @@ cudaError_t launch_attention(const AttnArgs& args, const AttnPlan& p, int* launc
   if (p.parts()) {
     const int64_t R = int64_t(a.T) * a.H;
     cfg.gridDim = dim3(static_cast<unsigned>(R));
-    const int join = p.slots() > (R <= 256 ? 8 : 16) ? 4 : p.slots() > 8 ? 2 : 1;      // groups of threads
+    const int join = p.slots() > (R <= 256 ? 8 : 32) ? 4 : p.slots() > 8 ? 2 : 1;      // groups of threads
     cfg.blockDim = dim3(128 * join);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
