@@ -938,7 +938,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_pair_kernel(AttnArgs a,
       if (n < 2) continue;
       const uint32_t valid = __ballot_sync(0xffffffffu, row >= 0);
       // keys: row lw * 4 + sub of this CTA's 32
-      bool ok = mbar_wait<true>(&sh.scores[ks], kphase, &sh.abort);
+      bool ok = mbar_wait_cluster(&sh.scores[ks], kphase, &sh.abort);
       if (!__all_sync(0xffffffffu, ok)) break;
       const int32_t rk = __shfl_sync(0xffffffffu, row, sub);
       const __nv_bfloat16* sk = static_cast<const __nv_bfloat16*>(kv.latent) + static_cast<int64_t>(max(rk, 0)) * kLatentDim + col * 8;
@@ -950,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_pair_kernel(AttnArgs a,
         cp_async16(dk + kLatentBlocks * 4096, static_cast<const __nv_bfloat16*>(kv.rope) + static_cast<int64_t>(max(rk, 0)) * kLatentRope + col * 8, rk >= 0);
       cp_async_arrive(&sh.keys[ks]);
       // values: the rows of the warp's eight keys, this CTA's half of the values
-      ok = mbar_wait<true>(&sh.used[vs], vphase, &sh.abort) && (n != kValueStages + 1 || mbar_wait<true>(&sh.moved, 0, &sh.abort));
+      ok = mbar_wait_cluster(&sh.used[vs], vphase, &sh.abort) && (n != kValueStages + 1 || mbar_wait<true>(&sh.moved, 0, &sh.abort));
       if (!__all_sync(0xffffffffu, ok)) break;
       if (lane == 0) {
         sh.valid[vs][rank][lw] = valid & 15;
@@ -983,12 +983,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_pair_kernel(AttnArgs a,
       if (rank == 0) {
         // ---------------------------------------------------------------- scores = Q K^T
         constexpr uint32_t idesc = make_idesc(1, 2 * kAttnRows, kAttnTile);
-        ok = tiles == 0 || mbar_wait<true>(&sh.queries, 0, &sh.abort);
+        ok = tiles == 0 || mbar_wait_cluster(&sh.queries, 0, &sh.abort);
         for (int i = 0; i < tiles && ok; ++i) {
           const int st = i & 1;
           const uint32_t phase = (i >> 1) & 1;
-          if (i >= 2) ok = mbar_wait<true>(&sh.taken[st], phase ^ 1, &sh.abort);
-          ok = ok && mbar_wait<true>(&sh.keys[st], phase, &sh.abort) && mbar_wait<true>(&sh.peer_keys[st], phase, &sh.abort);
+          if (i >= 2) ok = mbar_wait_cluster(&sh.taken[st], phase ^ 1, &sh.abort);
+          ok = ok && mbar_wait<true>(&sh.keys[st], phase, &sh.abort) && mbar_wait_cluster(&sh.peer_keys[st], phase, &sh.abort);
           if (!ok) break;
           fence_proxy_async_smem();
           tc_fence_after();
@@ -1019,7 +1019,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_pair_kernel(AttnArgs a,
         }
       }
       int alone = 0;
-      mbar_wait<true>(&sh.drained[0], 0, &alone);
+      mbar_wait_cluster(&sh.drained[0], 0, &alone);
     }
     __syncwarp();
   } else if (warp == kSecondWarp) {
@@ -1031,8 +1031,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_pair_kernel(AttnArgs a,
         // ---------------------------------------------------------------- output += P V
         constexpr uint32_t idesc = make_idesc(1, 2 * kAttnRows, 256) | kIdescBMnMajor;
         for (int i = 0; i < tiles; ++i) {
-          ok = mbar_wait<true>(&sh.values[st], phase, &sh.abort) && mbar_wait<true>(&sh.peer_values[st], phase, &sh.abort) &&
-               mbar_wait<true>(&sh.weights[i & 1], (i >> 1) & 1, &sh.abort);
+          ok = mbar_wait<true>(&sh.values[st], phase, &sh.abort) && mbar_wait_cluster(&sh.peer_values[st], phase, &sh.abort) &&
+               mbar_wait_cluster(&sh.weights[i & 1], (i >> 1) & 1, &sh.abort);
           if (!ok) break;
           fence_proxy_async_smem();
           tc_fence_after();
@@ -1063,7 +1063,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_pair_kernel(AttnArgs a,
         }
       }
       int alone = 0;
-      mbar_wait<true>(&sh.drained[1], 0, &alone);
+      mbar_wait_cluster(&sh.drained[1], 0, &alone);
     }
     __syncwarp();
   } else {
@@ -1112,9 +1112,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_pair_kernel(AttnArgs a,
     uint32_t phase = 0;
     for (int i = 0; i < tiles; ++i) {
       const int b = i & 1;
-      ok = ok && mbar_wait<true>(&sh.scores[b], (i >> 1) & 1, &sh.abort) && mbar_wait<true>(&sh.listed[st], phase, &sh.abort);
+      ok = ok && mbar_wait_cluster(&sh.scores[b], (i >> 1) & 1, &sh.abort) && mbar_wait<true>(&sh.listed[st], phase, &sh.abort);
       // the weights' place: the second product of the tile before last
-      if (ok && i >= 2) ok = mbar_wait<true>(&sh.used[(i - 2) % kValueStages], ((i - 2) / kValueStages) & 1, &sh.abort);
+      if (ok && i >= 2) ok = mbar_wait_cluster(&sh.used[(i - 2) % kValueStages], ((i - 2) / kValueStages) & 1, &sh.abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {                                         // the partner may be waiting: the barrier of every tile is kept
         named_barrier(1 + (warp & 1), 64);
@@ -1170,7 +1170,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_pair_kernel(AttnArgs a,
         st_shared16(place + (((half * 4 + c) ^ (r & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
       }
       if (rescale && i > 0) {
-        ok = mbar_wait<true>(&sh.used[(i - 1) % kValueStages], ((i - 1) / kValueStages) & 1, &sh.abort);
+        ok = mbar_wait_cluster(&sh.used[(i - 1) % kValueStages], ((i - 1) / kValueStages) & 1, &sh.abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) continue;
         tc_fence_after();

@@ -129,11 +129,38 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// Arrives on CTA `rank`'s barrier that corresponds to this CTA's `bar`.  What it announces is for the tensor cores: a read
-// of tensor memory that is done, or shared memory that a proxy fence has handed over; it carries no other writes with it
-// (a release for the whole cluster waits for every memory access of the thread, some 800 cycles here).
+// Arrives on CTA `rank`'s barrier that corresponds to this CTA's `bar`, releasing to the cluster what this thread has
+// written, or has seen written, to its CTA's shared memory.  The default scope is the CTA, and a release of every memory
+// access at cluster scope takes some 800 cycles; only shared memory is handed over, and the fence says so.
 __device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(smem_addr(bar), rank)) : "memory");
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(smem_addr(bar), rank))
+      : "memory");
+}
+// The counterpart: mbar_wait() on a barrier of this CTA on which another CTA of the cluster arrives.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  auto probe = [&] {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(kTryWaitSuspendNs)
+        : "memory");
+    return done != 0;
+  };
+  bool done = probe();
+  for (const long long t0 = clock64(); !done; done = probe()) {
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      *abort = 1;
+      return false;
+    }
+  }
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+  return true;
 }
 
 // ----------------------------------------------------------------------------- TMA
