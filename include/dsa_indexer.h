@@ -463,8 +463,9 @@ typedef struct {
  * result is the same, bit for bit, on every run.
  *   workspace  device, 256-byte aligned, dsa_sparse_attention_workspace_bytes() bytes (which may
  *              be 0), used until the call's kernels finish; or NULL for the stream's own, grown with
- *              cudaMalloc (graphs captured with NULL on one stream share it and must not run at the same
- *              time).  dsa_set_workspace does not apply here.
+ *              cudaMalloc (host threads may share the stream; graphs captured with NULL on one stream share
+ *              the workspace with that stream and must not run beside one another or beside its calls).
+ *              dsa_set_workspace does not apply here.
  */
 DSA_API dsa_status_t dsa_sparse_attention(const dsa_latent_query_t* q, const dsa_latent_cache_t* cache,
                                           const dsa_page_table_t* pages, const int32_t* seq_ids, const int32_t* idx,

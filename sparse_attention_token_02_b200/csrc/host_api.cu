@@ -160,6 +160,8 @@ struct Ctx {
   void* d_attn = nullptr;
   size_t attn_cap = 0;
   bool attn_frozen = false;       // a captured graph reads d_attn
+  std::vector<void*> attn_graveyard;   // earlier d_attn that a captured graph may still use
+  std::mutex attn_mu;             // held from the choice of d_attn until the call's last launch is enqueued
 };
 
 std::mutex g_mu;
@@ -1344,7 +1346,8 @@ int current_sms() {
   return n;
 }
 
-// Workspace of one attention call: the caller's, or the stream's own.
+// Workspace of one attention call: the caller's, or the stream's own, for which the caller of this holds attn_mu: another
+// host thread's call on the stream may neither replace the buffer nor put its parts there between this one's launches.
 dsa_status_t attention_parts(Ctx* c, size_t need, void* workspace, size_t workspace_bytes, void** out) {
   *out = nullptr;
   if (need == 0) return DSA_OK;
@@ -1358,12 +1361,11 @@ dsa_status_t attention_parts(Ctx* c, size_t need, void* workspace, size_t worksp
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   DSA_CUDA_TRY(cudaStreamIsCapturing(c->stream, &cap), "cudaStreamIsCapturing");
   const bool capturing = cap != cudaStreamCaptureStatusNone;
-  std::lock_guard<std::mutex> lk(g_mu);
   if (need > c->attn_cap) {
     AllowAllocation allow;
     if (c->d_attn) {
       if (c->attn_frozen || capturing) {              // a graph may read it, or work that cannot be waited for
-        c->graveyard.push_back(c->d_attn);
+        c->attn_graveyard.push_back(c->d_attn);
       } else {
         DSA_CUDA_TRY(cudaStreamSynchronize(c->stream), "cudaStreamSynchronize");
         cudaFree(c->d_attn);
@@ -1404,8 +1406,10 @@ dsa_status_t run_attention(const dsa_latent_query_t* q, AttnArgs* a, int64_t sha
   if (st != DSA_OK) return st;
   AllowAllocation allow;                               // a kernel's first use may come inside a capture
   const AttnPlan p = plan_attention(q->T, q->H, shared_keys, own_keys, a->kv.fp8, current_sms());
-  if ((st = attention_parts(c, attention_workspace(p, q->T, q->H, shared_keys), workspace, workspace_bytes, &a->workspace)) != DSA_OK)
-    return st;
+  const size_t need = attention_workspace(p, q->T, q->H, shared_keys);
+  std::unique_lock<std::mutex> own(c->attn_mu, std::defer_lock);
+  if (need > 0 && !workspace) own.lock();
+  if ((st = attention_parts(c, need, workspace, workspace_bytes, &a->workspace)) != DSA_OK) return st;
   a->err = c->d_err;
   int launched = 0;
   const cudaError_t e = launch_attention(*a, p, &launched, stream);

@@ -1,0 +1,73 @@
+"""The layer's operators on the GPU where calls meet: host threads, captures, and rows whose neighbours hold anything.
+
+Results are compared with the same call made alone, bit for bit, or with oracle/layer.py in fp64 under the tolerances
+that tests/test_gpu_layer.py derives.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+from sparse_attention_token_02_b200 import _lib, api
+from .test_gpu_layer import SM, check_token, f64, gen, make_cache, queries
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    api.dsa_version()
+    yield
+    api.dsa_check_device_errors()
+
+
+def test_threads_on_one_stream_share_its_workspace():
+    # calls without a workspace, in parts: neither thread's parts may land between the other's kernels, and the second
+    # sizes need a larger buffer than the first left behind
+    cache, _ = make_cache(4096, 64, False, 1)
+    table = torch.arange(64, dtype=torch.int32).view(1, 64).cuda()
+    lib, stream = _lib.load(), torch.cuda.Stream()
+    view, pages = cache.c(), _lib.PageTable(table.data_ptr(), 1, 64)
+
+    def prepare(T, prefix, n):
+        ql, qr = (x.cuda() for x in queries(T, 16, T))
+        ids, lens = torch.zeros(T, dtype=torch.int32).cuda(), torch.full((T,), n, dtype=torch.int32).cuda()
+        want = api.dsa_prefix_attention(ql, qr, cache, table, ids, lens, SM, prefix_len=prefix, max_keys=n)[0]
+        assert lib.dsa_prefix_attention_workspace_bytes(T, 16, prefix, n, _lib.DSA_BF16) > 0
+        q = _lib.LatentQuery(ql.data_ptr(), ql.stride(0), ql.stride(1), qr.data_ptr(), qr.stride(0), qr.stride(1), T, 16)
+        return (ql, qr, ids, lens), q, prefix, n, want
+
+    calls = [prepare(T, prefix, n) for T, prefix, n in ((2, 500, 600), (40, 3000, 4096), (5, 1000, 1500), (64, 3500, 4096))]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(order):
+        try:
+            for _ in range(25):
+                outs = {}
+                for i in order:
+                    (_, _, ids, lens), q, prefix, n, want = calls[i]
+                    outs[i] = torch.empty_like(want)
+                    _lib.check(lib.dsa_prefix_attention(ctypes.byref(q), ctypes.byref(view), ctypes.byref(pages), ids.data_ptr(),
+                                                        lens.data_ptr(), prefix, 0, n, SM, outs[i].data_ptr(), None, None, 0,
+                                                        stream.cuda_stream))
+                stream.synchronize()
+                if any(not torch.equal(outs[i], calls[i][4]) for i in order):
+                    bad.append(order)
+        except Exception as e:                               # reported by the main thread
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=(o,)) for o in ([0, 1], [2, 3], [3, 0])]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+    api.dsa_check_device_errors(stream)
