@@ -479,7 +479,8 @@ DSA_API dsa_status_t dsa_sparse_attention(const dsa_latent_query_t* q, const dsa
  * keys are read once for each 64 rows (token, head) of the whole batch; the rest per token.  prefix_len = 0
  * is plain paged attention, the dense alternative while a sequence is no longer than top_k.
  *   key_lens   device int32 [T], each at most max_keys (a longer one is cut there and reported); one below
- *              prefix_len reads that many of the shared positions, one below 1 nothing (zeros and -inf)
+ *              prefix_len reads that many of the shared positions, one below 1 nothing (zeros and -inf);
+ *              what lies behind a token's last position does not reach it, NaN and infinities included
  *   max_keys   host bound on key_lens; the work is cut to it, so a tight one is faster
  * The other arguments are those of dsa_sparse_attention; workspace: dsa_prefix_attention_workspace_bytes.
  */

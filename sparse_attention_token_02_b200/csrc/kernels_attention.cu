@@ -140,6 +140,24 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t src) {
   return v;
 }
 
+// Zeroes what is not finite in `bytes` of bf16 values from `base`, by the 128 threads of the softmax warps.  A key that a row
+// may not read has weight 0 there, but 0 * NaN would still reach the row's output; rows that do read it have a score,
+// and with it every weight, that is not finite already.  (Minus infinity aside: that key then has weight 0 for them.)
+__device__ __forceinline__ void keep_finite(uint32_t base, uint32_t bytes, int thread) {
+#pragma unroll 1
+  for (uint32_t at = base + thread * 16; at < base + bytes; at += 128 * 16) {
+    const uint4 u = ld_shared16(at);
+    uint32_t w[4] = {u.x, u.y, u.z, u.w}, any = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t wild = __vcmpeq2(w[i] & 0x7F807F80u, 0x7F807F80u);   // an exponent of ones, in either half
+      w[i] &= ~wild;
+      any |= wild;
+    }
+    if (any) st_shared16(at, make_uint4(w[0], w[1], w[2], w[3]));
+  }
+}
+
 struct __align__(8) Shared {
   uint64_t full[kStages][2];    // a half of a tile's keys is in shared memory (the second half with the rotated part)
   uint64_t listed[kStages];     // `valid` of a tile is written
@@ -152,6 +170,7 @@ struct __align__(8) Shared {
   uint32_t tmem;
   int abort;
   int32_t key_end;
+  int32_t first_limit;          // the smallest limit of a row that has keys here, where rows of several tokens meet
   int32_t limit[kAttnRows];     // keys at or past a row's limit are not its own
   float inv[kAttnRows];         // 1 / the row's sum (0 for a row without keys)
   float lse2[kAttnRows];        // the base-2 log of the row's sum
@@ -228,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       mbar_init(&sh.queries, kSoftmaxWarps);
       sh.abort = 0;
       sh.key_end = 0;
+      sh.first_limit = 0x7FFFFFFF;
       fence_barrier_init();
     }
     __syncwarp();
@@ -249,6 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
       }
       sh.limit[tid] = n;
       atomicMax(&sh.key_end, min(n, k1));
+      if (n > k0) atomicMin(&sh.first_limit, n);
     }
   } else {
     seq = token_seq(a, token);
@@ -273,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
     }
   }
   __syncthreads();
-  const int32_t key_end = sh.key_end;
+  const int32_t key_end = sh.key_end, first_limit = sh.first_limit;
   const int tiles = key_end > k0 ? (key_end - k0 + kAttnTile - 1) / kAttnTile : 0;
   tc_fence_after();
 
@@ -629,6 +650,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
         }
         tmem_st_wait();
       }
+      if (first_limit < min(kb + kAttnTile, key_end)) {  // a row that ended before the tile's last key
+        ok = mbar_wait<true>(&sh.full[st][0], phase, &sh.abort) && mbar_wait<true>(&sh.full[st][1], phase, &sh.abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        keep_finite(smem + kOffK + st * kStage, kLatentBlocks * kBlock, tid);
+      }
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
@@ -794,7 +821,7 @@ struct __align__(8) SharedPair {
   uint64_t drained[2];
   uint32_t tmem;
   int abort;
-  int32_t key_end;
+  int32_t key_end, first_limit;
   int32_t limit[kAttnRows];
   float inv[kAttnRows];
   float top[2][2][kAttnRows];   // a tile's maxima over either half of its keys, two tiles in turn
@@ -855,6 +882,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_pair_kernel(AttnArgs a,
       mbar_init(&sh.moved, kSoftmaxWarps);
       sh.abort = 0;
       sh.key_end = 0;
+      sh.first_limit = 0x7FFFFFFF;
       fence_barrier_init();
     }
     __syncwarp();
@@ -877,6 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_pair_kernel(AttnArgs a,
       }
       if (tid / kAttnRows == rank) sh.limit[tid % kAttnRows] = n;
       atomicMax(&sh.key_end, min(n, k1));
+      if (n > k0) atomicMin(&sh.first_limit, n);
     }
   } else {
     seq = token_seq(a, token);
@@ -900,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_pair_kernel(AttnArgs a,
     }
   }
   __syncthreads();
-  const int32_t key_end = sh.key_end;
+  const int32_t key_end = sh.key_end, first_limit = sh.first_limit;
   const int tiles = key_end > k0 ? (key_end - k0 + kAttnTile - 1) / kAttnTile : 0;
   tc_fence_after();
 
@@ -1184,6 +1213,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_pair_kernel(AttnArgs a,
           tmem_st_32x32b_x32(quadrant + kTmemO + c, o);
         }
         tmem_st_wait();
+      }
+      if (first_limit < min(k0 + (i + 1) * kAttnTile, key_end)) {   // a row of either CTA that ended before the tile's last key
+        ok = mbar_wait<true>(&sh.values[st], phase, &sh.abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) continue;
+        keep_finite(smem + kPairV + st * kPairValues, kPairValues, tid);
       }
       fence_proxy_async_smem();
       tc_fence_before();

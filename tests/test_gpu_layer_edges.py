@@ -71,3 +71,38 @@ def test_threads_on_one_stream_share_its_workspace():
         t.join()
     assert not bad
     api.dsa_check_device_errors(stream)
+
+
+@pytest.mark.parametrize("T,H,prefix,own,fp8,d_r", [
+    (5, 16, 500, 40, False, 64), (6, 24, 1000, 64, False, 0), (9, 96, 700, 30, False, 64), (64, 16, 4096, 40, False, 64),
+    (16, 24, 9000, 100, False, 64), (5, 24, 1000, 64, True, 64), (40, 16, 8000, 30, True, 64), (9, 128, 3000, 10, False, 64),
+])
+def test_prefix_a_token_does_not_read_may_hold_anything(T, H, prefix, own, fp8, d_r):
+    # tokens that end inside the shared prefix, beside others that read on: what lies behind their end must not reach
+    # them, though all are rows of the same products (one CTA, pairs, FP8 as it is and expanded, a token's own items)
+    page = 64
+    full, pages = prefix // page, -(-(prefix + own) // page) + 1
+    num_pages = full + T * (pages - full)
+    cache, vals = make_cache(num_pages * page, page, fp8, T, d_r)
+    table = torch.cat([torch.arange(full).expand(T, full), full + torch.arange(T * (pages - full)).view(T, pages - full)], 1).to(torch.int32)
+    n = prefix // 2 - 5
+    behind = [n, n + 1, n + 9, n + 64, n + 130, full * page - 1]
+    nan, inf = (0x7F, 0xFF) if fp8 else (float("nan"), float("inf"))
+    for j, p in enumerate(behind):
+        cache.latent[p, (j * 97 + 3) % 512] = nan
+        cache.latent[p, 511] = inf
+        cache.latent[p + 1, 200 + j] = -inf if not fp8 else nan
+    if d_r:
+        cache.rope[n:full * page:50] = float("nan")
+    lens = torch.full((T,), prefix + own, dtype=torch.int32)
+    lens[1], lens[2], lens[3], lens[4] = n, 0, n, n - 100
+    ids = torch.arange(T, dtype=torch.int32)
+    ql, qr = queries(T, H, 7)
+    out, lse = api.dsa_prefix_attention(ql.cuda(), qr.cuda() if d_r else None, cache, table.cuda(), ids.cuda(), lens.cuda(), SM,
+                                        prefix_len=full * page, max_keys=prefix + own)
+    api.dsa_check_device_errors()
+    q = f64(torch.cat([ql, qr], 2) if d_r else ql)
+    for t in (1, 2, 3, 4):
+        check_token(f64(out)[t], f64(lse)[t], q[t], vals[:int(lens[t])], SM, t)
+    reads = [t for t in range(T) if t not in (1, 2, 3, 4)]
+    assert torch.isnan(out[reads]).all() and torch.isnan(lse[reads]).all()
