@@ -7,6 +7,9 @@ that tests/test_gpu_layer.py derives.
 from __future__ import annotations
 
 import ctypes
+import os
+import subprocess
+import sys
 import threading
 
 import numpy as np
@@ -106,3 +109,41 @@ def test_prefix_a_token_does_not_read_may_hold_anything(T, H, prefix, own, fp8, 
         check_token(f64(out)[t], f64(lse)[t], q[t], vals[:int(lens[t])], SM, t)
     reads = [t for t in range(T) if t not in (1, 2, 3, 4)]
     assert torch.isnan(out[reads]).all() and torch.isnan(lse[reads]).all()
+
+
+FIRST = """
+import torch
+from sparse_attention_token_02_b200 import api
+
+cache = api.LatentCache.empty(64, 64, fp8={fp8})
+cache.rope.normal_()
+table = torch.arange(64, dtype=torch.int32, device="cuda").view(1, 64)
+ids, lens = (torch.full(({T},), n, dtype=torch.int32, device="cuda") for n in (0, 4096))
+ql, qr = torch.randn({T}, {H}, 512, device="cuda").bfloat16(), torch.randn({T}, {H}, 64, device="cuda").bfloat16()
+idx = torch.arange(2048, dtype=torch.int32, device="cuda").repeat({T}, 1)
+x, w = torch.randn(400, 1024, device="cuda"), torch.ones(1024, device="cuda")
+torch.cuda.synchronize()
+
+
+def call():
+    return [*api.dsa_prefix_attention(ql, qr, cache, table, ids, lens, 0.1, prefix_len=3000, max_keys=4096),
+            *api.dsa_sparse_attention(ql, qr, cache, table, ids, idx, 0.1), *api.dsa_rmsnorm_fp8(x, w)[:2]]
+
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = call()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, call()))
+api.dsa_check_device_errors()
+print("equal")
+"""
+
+
+@pytest.mark.parametrize("T,H,fp8", [(1, 128, False), (40, 16, False), (30, 128, True)])
+def test_a_process_first_call_may_be_captured(T, H, fp8):
+    # nothing has asked for a workspace, a cluster's room or a kernel before the capture begins
+    r = subprocess.run([sys.executable, "-c", FIRST.format(T=T, H=H, fp8=fp8)], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "equal" in r.stdout, r.stderr[-2000:]
