@@ -214,6 +214,8 @@ cudaError_t launch_latent_append(const LatentAppendArgs& a, const RopeParams& r,
 // Own items: rows of one token against chunk `slot` of that token's own keys.
 constexpr int kAttnRows = 64;          // rows per work item
 constexpr int kAttnTile = 64;          // keys per tile; chunks are whole tiles
+constexpr int kMaxCluster = 16;        // parts of a row that a cluster joins
+constexpr int kMaxSlots = 256;         // and that the second kernel does
 struct AttnPlan {
   int32_t shared_groups, shared_slots, shared_chunk;
   int32_t own_groups, own_slots, own_chunk;       // own_groups: row groups of one token
@@ -248,6 +250,7 @@ struct AttnArgs {
   int* err;
 };
 // keys: own_keys bounds the keys of each token's own part
+int cluster_room(int cluster, int sms, bool* answered);
 AttnPlan plan_attention(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, bool fp8, int sms);
 size_t attention_workspace(const AttnPlan& p, int64_t T, int32_t H, int64_t shared_keys);
 // returns the number of kernels launched through *launched

@@ -1,8 +1,12 @@
 """The layer's operators without a GPU: what their sources, builds and bindings promise beyond test_layer_cpu.py."""
 
+import ctypes
 import glob
 import os
 import re
+import subprocess
+
+import pytest
 
 from sparse_attention_token_02_b200 import build
 
@@ -34,3 +38,48 @@ def test_waits_for_a_neighbours_arrivals_acquire_at_cluster_scope():
     assert {bar for _, bar in waits} >= {"scores", "taken", "weights", "queries", "peer_keys", "peer_values", "used", "drained"}
     for call, bar in waits:
         assert call == ("mbar_wait" if bar in own else "mbar_wait_cluster"), (call, bar)
+
+
+FAKE_DEVICE = """
+#include <cuda_runtime.h>
+#include "internal.h"
+static int device = 0, rooms[2] = {16, 16};
+extern "C" cudaError_t cudaGetDevice(int* d) { *d = device; return cudaSuccess; }
+namespace dsa {
+int cluster_room(int cluster, int, bool* answered) {     // CTAs in clusters of up to rooms[device]; negative: no answer
+  if (rooms[device] < 0) *answered = false;
+  return rooms[device] >= cluster ? 148 / cluster * cluster : 0;
+}
+}
+extern "C" void set(int d, int room0, int room1) { device = d; rooms[0] = room0; rooms[1] = room1; }
+extern "C" int cluster_of(long T, int H, long own) { return dsa::plan_attention(T, H, 0, own, false, 148).cluster; }
+"""
+
+
+@pytest.fixture(scope="module")
+def planner(tmp_path_factory):
+    """The planner of attention calls on a fake of the device's answers."""
+    tmp = tmp_path_factory.mktemp("plan")
+    (tmp / "fake.cpp").write_text(FAKE_DEVICE)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(build.nvcc())), "include")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-fPIC", "-shared", f"-I{cuda}", f"-I{build.INCLUDE}", f"-I{build.CSRC}", "-x", "c++",
+                    os.path.join(build.CSRC, "attention_plan.cu"), str(tmp / "fake.cpp"), "-o", str(tmp / "plan.so")], check=True)
+    return ctypes.CDLL(str(tmp / "plan.so"))
+
+
+def test_a_plan_belongs_to_its_device(planner):
+    # two devices with as many SMs, only the first with room for clusters: one query over 2048 keys is cut into
+    # a cluster there and through memory on the other, whichever was asked before
+    planner.set(0, 16, 0)
+    assert planner.cluster_of(1, 128, 2048) > 1
+    planner.set(1, 16, 0)
+    assert planner.cluster_of(1, 128, 2048) == 1
+    planner.set(0, 16, 0)
+    assert planner.cluster_of(1, 128, 2048) > 1
+
+
+def test_a_plan_without_the_devices_answer_is_not_kept(planner):
+    planner.set(0, -1, 0)
+    assert planner.cluster_of(2, 128, 2048) == 1
+    planner.set(0, 16, 0)
+    assert planner.cluster_of(2, 128, 2048) > 1
