@@ -44,6 +44,12 @@ double double_of(PyObject* o) {
   return v;
 }
 
+int truth_of(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  require(v >= 0);
+  return v;
+}
+
 // The call's tensors: on the current device, ordinary ones.
 struct Call {
   const int device = c10::cuda::current_device();
@@ -203,7 +209,7 @@ PyObject* append(PyObject* const* a) {
     require(kr->dim() == 2 && kr->size(0) == c.size(0) && kr->size(1) == 64 && kr->stride(1) == 1 && kr->scalar_type() == c.scalar_type());
   }
   const int32_t *seq = call.ints(a[7], c.size(0)), *pos = call.ints(a[8], c.size(0));
-  const dsa_rope_t rope{int32_of(a[9]), PyObject_IsTrue(a[11]) ? 1 : 0, double_of(a[10])};
+  const dsa_rope_t rope{int32_of(a[9]), truth_of(a[11]), double_of(a[10])};
   const dsa_dtype_t code = float_code(c);
   library_call([&] {
     return lib.append(&cache, &table, c.data_ptr(), c.stride(0), address(kr), kr ? kr->stride(0) : 0, code, seq, pos,

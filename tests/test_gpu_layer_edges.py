@@ -147,3 +147,17 @@ def test_a_process_first_call_may_be_captured(T, H, fp8):
     r = subprocess.run([sys.executable, "-c", FIRST.format(T=T, H=H, fp8=fp8)], capture_output=True, text=True, timeout=300,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and "equal" in r.stdout, r.stderr[-2000:]
+
+
+def test_an_argument_whose_truth_raises_is_an_error():
+    class Undecided:
+        def __bool__(self):
+            raise ValueError("undecided")
+
+    cache = api.LatentCache.empty(2, 64)
+    table, ids = torch.arange(2, dtype=torch.int32).view(1, 2).cuda(), torch.zeros(3, dtype=torch.int32).cuda()
+    new = torch.ones(3, 576, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="undecided"):
+        api.dsa_latent_append_rope(cache, table, new[:, :512], new[:, 512:], ids, torch.arange(3, dtype=torch.int32).cuda(),
+                                   interleaved=Undecided())
+    assert not cache.latent.any() and not cache.rope.any()
