@@ -70,10 +70,13 @@ struct Call {
   const int32_t* ints(PyObject* o, int64_t n) const {
     const at::Tensor& t = tensor(o);
     require(t.scalar_type() == at::kInt && t.dim() == 1 && t.size(0) == n);
-    return static_cast<const int32_t*>(t.data_ptr());
+    return static_cast<const int32_t*>(t.const_data_ptr());
   }
 };
 
+// Where a tensor that is only read lies: a lazy clone stays one, where data_ptr() would copy it first.
+void* read_only(const at::Tensor& t) { return const_cast<void*>(t.const_data_ptr()); }
+void* read_only(const at::Tensor* t) { return t ? read_only(*t) : nullptr; }
 void* address(const at::Tensor* t) { return t ? t->data_ptr() : nullptr; }
 
 dsa_dtype_t float_code(const at::Tensor& t) {
@@ -103,7 +106,7 @@ struct Result {
   PyObject* object() const { return given ? Py_NewRef(given) : THPVariable_Wrap(made); }
 };
 
-dsa_latent_cache_t cache_of(const Call& call, PyObject* latent, PyObject* rope, PyObject* scale, PyObject* page_size) {
+dsa_latent_cache_t cache_of(const Call& call, PyObject* latent, PyObject* rope, PyObject* scale, PyObject* page_size, bool written) {
   const at::Tensor& l = call.tensor(latent);
   const at::Tensor* r = call.optional(rope);
   const at::Tensor* s = call.optional(scale);
@@ -116,9 +119,9 @@ dsa_latent_cache_t cache_of(const Call& call, PyObject* latent, PyObject* rope, 
             s->numel() == l.size(0));
   if (r) require(r->scalar_type() == at::kBFloat16 && r->dim() == 2 && r->size(0) == l.size(0) && r->size(1) <= 4096);
   dsa_latent_cache_t c{};
-  c.latent = l.data_ptr();
-  c.scale = fp8 ? static_cast<float*>(s->data_ptr()) : nullptr;
-  c.rope = address(r);
+  c.latent = written ? l.data_ptr() : read_only(l);
+  c.scale = fp8 ? static_cast<float*>(written ? s->data_ptr() : read_only(s)) : nullptr;
+  c.rope = written ? address(r) : read_only(r);
   c.num_pages = static_cast<int32_t>(l.size(0) / page);
   c.page_size = page;
   c.d_c = static_cast<int32_t>(l.size(1));
@@ -131,7 +134,7 @@ dsa_page_table_t table_of(const Call& call, PyObject* o) {
   const at::Tensor& t = call.tensor(o);
   require(t.scalar_type() == at::kInt && t.dim() == 2 && t.size(0) <= std::numeric_limits<int32_t>::max() &&
           t.size(1) <= std::numeric_limits<int32_t>::max());
-  return dsa_page_table_t{static_cast<const int32_t*>(t.data_ptr()), static_cast<int32_t>(t.size(0)), static_cast<int32_t>(t.size(1))};
+  return dsa_page_table_t{static_cast<const int32_t*>(t.const_data_ptr()), static_cast<int32_t>(t.size(0)), static_cast<int32_t>(t.size(1))};
 }
 
 dsa_latent_query_t query_of(const Call& call, PyObject* latent, PyObject* rope, bool rotated) {
@@ -139,7 +142,7 @@ dsa_latent_query_t query_of(const Call& call, PyObject* latent, PyObject* rope, 
   require(l.scalar_type() == at::kBFloat16 && l.dim() == 3 && l.size(2) == 512 && l.stride(2) == 1 && l.size(0) >= 1 &&
           l.size(0) <= std::numeric_limits<int32_t>::max() && l.size(1) >= 1 && l.size(1) <= 128);
   dsa_latent_query_t q{};
-  q.latent = l.data_ptr();
+  q.latent = l.const_data_ptr();
   q.latent_stride_t = l.stride(0);
   q.latent_stride_h = l.stride(1);
   q.T = static_cast<int32_t>(l.size(0));
@@ -148,20 +151,26 @@ dsa_latent_query_t query_of(const Call& call, PyObject* latent, PyObject* rope, 
     const at::Tensor& r = call.tensor(rope, false);
     require(r.scalar_type() == at::kBFloat16 && r.dim() == 3 && r.size(0) == l.size(0) && r.size(1) == l.size(1) &&
             r.size(2) == 64 && r.stride(2) == 1);
-    q.rope = r.data_ptr();
+    q.rope = r.const_data_ptr();
     q.rope_stride_t = r.stride(0);
     q.rope_stride_h = r.stride(1);
   }
   return q;
 }
 
-// Another thread may run Python while a launch waits for room in the stream.
-template <class F>
-void library_call(F&& f) {
+// Another thread may run Python while a launch waits for room in the stream.  The arguments are there before the lock is
+// given up (taking a result's address may still copy a lazy clone, which can fail), and it is taken back however f ends.
+template <class F, class... Args>
+void library_call(F f, Args... args) {
+  struct Unlocked {
+    PyThreadState* const thread = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(thread); }
+  };
   dsa_status_t status;
-  Py_BEGIN_ALLOW_THREADS
-  status = f();
-  Py_END_ALLOW_THREADS
+  {
+    const Unlocked unlocked;
+    status = f(args...);
+  }
   require(status == DSA_OK);
 }
 
@@ -180,12 +189,10 @@ PyObject* rmsnorm(PyObject* const* a) {
   const dsa_dtype_t code = float_code(x), weight_code = float_code(w);
   const Result codes(call, a[6], {rows, d}, x.options().dtype(at::kByte));
   const Result scale(call, a[7], {rows, groups}, x.options().dtype(at::kFloat));
-  auto run = [&](void* residual_out) {
-    library_call([&] {
-      return lib.rmsnorm(x.data_ptr(), code, x.stride(0), address(residual), residual_out, w.data_ptr(), weight_code, rows,
-                         static_cast<int32_t>(d), eps, group, static_cast<uint8_t*>(codes.ptr), static_cast<float*>(scale.ptr),
-                         address(normed), call.stream());
-    });
+  auto run = [&](void* residual_out) {                   // the residual's address after the result's: they may be one tensor
+    library_call(lib.rmsnorm, read_only(x), code, x.stride(0), read_only(residual), residual_out, read_only(w), weight_code, rows,
+                 static_cast<int32_t>(d), eps, group, static_cast<uint8_t*>(codes.ptr), static_cast<float*>(scale.ptr),
+                 address(normed), call.stream());
   };
   if (!residual) {
     run(nullptr);
@@ -199,7 +206,7 @@ PyObject* rmsnorm(PyObject* const* a) {
 // latent, rope, scale, page_size, page_table, c_new, kr_new, seq_ids, positions, rope_dim, base, interleaved
 PyObject* append(PyObject* const* a) {
   const Call call;
-  const dsa_latent_cache_t cache = cache_of(call, a[0], a[1], a[2], a[3]);
+  const dsa_latent_cache_t cache = cache_of(call, a[0], a[1], a[2], a[3], true);
   const dsa_page_table_t table = table_of(call, a[4]);
   const at::Tensor& c = call.tensor(a[5], false);
   require(c.dim() == 2 && c.size(0) >= 1 && c.size(0) <= std::numeric_limits<int32_t>::max() && c.size(1) == 512 && c.stride(1) == 1);
@@ -211,10 +218,8 @@ PyObject* append(PyObject* const* a) {
   const int32_t *seq = call.ints(a[7], c.size(0)), *pos = call.ints(a[8], c.size(0));
   const dsa_rope_t rope{int32_of(a[9]), truth_of(a[11]), double_of(a[10])};
   const dsa_dtype_t code = float_code(c);
-  library_call([&] {
-    return lib.append(&cache, &table, c.data_ptr(), c.stride(0), address(kr), kr ? kr->stride(0) : 0, code, seq, pos,
-                      static_cast<int32_t>(c.size(0)), &rope, call.stream());
-  });
+  library_call(lib.append, &cache, &table, read_only(c), c.stride(0), read_only(kr), kr ? kr->stride(0) : 0, code, seq, pos,
+               static_cast<int32_t>(c.size(0)), &rope, call.stream());
   return Py_NewRef(Py_True);
 }
 
@@ -241,7 +246,7 @@ struct Outputs {
 // q_latent, q_rope, latent, rope, scale, page_size, page_table, seq_ids, idx, sm_scale, out, lse, workspace
 PyObject* sparse(PyObject* const* a) {
   const Call call;
-  const dsa_latent_cache_t cache = cache_of(call, a[2], a[3], a[4], a[5]);
+  const dsa_latent_cache_t cache = cache_of(call, a[2], a[3], a[4], a[5], false);
   const dsa_latent_query_t q = query_of(call, a[0], a[1], cache.rope != nullptr);
   const dsa_page_table_t table = table_of(call, a[6]);
   const int32_t* seq = call.ints(a[7], q.T);
@@ -251,10 +256,8 @@ PyObject* sparse(PyObject* const* a) {
   const float scale = static_cast<float>(double_of(a[9]));
   const size_t need = a[12] == Py_None ? lib.sparse_bytes(q.T, q.H, k, cache.dtype) : 0;
   const Outputs o(call, THPVariable_Unpack(a[0]), q, a[10], a[11], a[12], need);
-  library_call([&] {
-    return lib.sparse(&q, &cache, &table, seq, static_cast<const int32_t*>(idx.data_ptr()), k, scale, o.out.ptr,
-                      static_cast<float*>(o.lse.ptr), o.workspace, o.bytes, call.stream());
-  });
+  library_call(lib.sparse, &q, &cache, &table, seq, static_cast<const int32_t*>(read_only(idx)), k, scale, o.out.ptr,
+               static_cast<float*>(o.lse.ptr), o.workspace, o.bytes, call.stream());
   return o.pair();
 }
 
@@ -262,7 +265,7 @@ PyObject* sparse(PyObject* const* a) {
 // sm_scale, out, lse, workspace
 PyObject* prefix(PyObject* const* a) {
   const Call call;
-  const dsa_latent_cache_t cache = cache_of(call, a[2], a[3], a[4], a[5]);
+  const dsa_latent_cache_t cache = cache_of(call, a[2], a[3], a[4], a[5], false);
   const dsa_latent_query_t q = query_of(call, a[0], a[1], cache.rope != nullptr);
   const dsa_page_table_t table = table_of(call, a[6]);
   const int32_t *seq = call.ints(a[7], q.T), *lens = call.ints(a[8], q.T);
@@ -273,10 +276,8 @@ PyObject* prefix(PyObject* const* a) {
   const float scale = static_cast<float>(double_of(a[12]));
   const size_t need = a[15] == Py_None ? lib.prefix_bytes(q.T, q.H, prefix_len, max_keys, cache.dtype) : 0;
   const Outputs o(call, THPVariable_Unpack(a[0]), q, a[13], a[14], a[15], need);
-  library_call([&] {
-    return lib.prefix(&q, &cache, &table, seq, lens, prefix_len, prefix_seq, max_keys, scale, o.out.ptr,
-                      static_cast<float*>(o.lse.ptr), o.workspace, o.bytes, call.stream());
-  });
+  library_call(lib.prefix, &q, &cache, &table, seq, lens, prefix_len, prefix_seq, max_keys, scale, o.out.ptr,
+               static_cast<float*>(o.lse.ptr), o.workspace, o.bytes, call.stream());
   return o.pair();
 }
 

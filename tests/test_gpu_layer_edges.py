@@ -161,3 +161,30 @@ def test_an_argument_whose_truth_raises_is_an_error():
         api.dsa_latent_append_rope(cache, table, new[:, :512], new[:, 512:], ids, torch.arange(3, dtype=torch.int32).cuda(),
                                    interleaved=Undecided())
     assert not cache.latent.any() and not cache.rope.any()
+
+
+LAZY = """
+import torch
+from sparse_attention_token_02_b200 import api
+
+x, w = torch.randn(1 << 15, 8192, dtype=torch.bfloat16, device="cuda"), torch.ones(8192, device="cuda")
+want = api.dsa_rmsnorm_fp8(x, w)[0]
+lazy = x._lazy_clone()                                       # copied when it is written, or its address asked for
+total = torch.cuda.get_device_properties(0).total_memory
+torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + x.numel() * 1.25) / total)
+got = api.dsa_rmsnorm_fp8(lazy, w)[0]                        # there is room for the results, not for a copy
+assert torch._C._is_cow_tensor(lazy) and all(torch.equal(got[i:i + 4096], want[i:i + 4096]) for i in range(0, 1 << 15, 4096))
+torch.cuda.set_per_process_memory_fraction(1.0)
+lazy = x._lazy_clone()
+out = api.dsa_rmsnorm_fp8(x, w, residual=lazy, residual_out=lazy)[2]       # written: its own now
+assert out is lazy and not torch._C._is_cow_tensor(lazy) and torch.equal(api.dsa_rmsnorm_fp8(x, w)[0], want)
+assert torch.equal(out[:64], (x[:64].float() + x[:64].float()).bfloat16())
+print("equal")
+"""
+
+
+def test_what_is_only_read_is_not_copied_first():
+    # a copy inside a call could run out of memory there, while other threads run Python
+    r = subprocess.run([sys.executable, "-c", LAZY], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "equal" in r.stdout, (r.returncode, r.stdout, r.stderr[-2000:])
