@@ -446,6 +446,13 @@ def _int32(name, t, *shape):
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
 
+def _fit(**numbers):
+    """What becomes an int32 of the C call must be one: ctypes would keep the low 32 bits."""
+    for name, v in numbers.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{name} must fit 32 bits, got {v}")
+
+
 def dsa_rmsnorm_fp8(x, weight, eps=1e-6, residual=None, group=128, residual_out=None, codes=None, scale=None,
                     normed=None, stream=None):
     """RMS norm of ``x`` [rows, d] (bf16 / fp32, rows may be strided) with the residual's addition, quantised to
@@ -463,6 +470,7 @@ def dsa_rmsnorm_fp8(x, weight, eps=1e-6, residual=None, group=128, residual_out=
         raise ValueError("weight must hold d values")
     if group != 128 and group != 0:
         raise ValueError("group must be 0 (one scale per row) or 128")
+    _fit(d=d)
     guard = _elsewhere(x, stream)
     if guard is not None:
         with guard:
@@ -499,6 +507,7 @@ def _address(t):
 def _page_table(page_table) -> _lib.PageTable:
     if page_table.dtype is not torch.int32 or page_table.dim() != 2:
         raise TypeError("page_table must be int32 [num_seqs, max_pages]")
+    _fit(num_seqs=page_table.shape[0], max_pages=page_table.shape[1])
     return _lib.PageTable(page_table.data_ptr(), *page_table.shape)
 
 
@@ -525,13 +534,15 @@ def dsa_latent_append_rope(cache: LatentCache, page_table, c_new, kr_new, seq_id
         kr_new = None
     _int32("seq_ids", seq_ids, n)
     _int32("positions", positions, n)
+    table, rope_dim = _page_table(page_table), 64 if rope_dim is None else int(rope_dim)
+    _fit(n=n, rope_dim=rope_dim)
     guard = _elsewhere(cache.latent, stream)
     if guard is not None:
         with guard:
             return dsa_latent_append_rope(cache, page_table, c_new, kr_new, seq_ids, positions, rope_dim, base, interleaved)
     _one_device(cache.latent, cache.rope, cache.scale, cache.latent, page_table, seq_ids, positions)
     _one_device(cache.latent, c_new, kr_new, contiguous=False)
-    check(_lib.load().dsa_latent_append_rope(cache.c(), _page_table(page_table), c_new.data_ptr(), c_new.stride(0),
+    check(_lib.load().dsa_latent_append_rope(cache.c(), table, c_new.data_ptr(), c_new.stride(0),
                                              _address(kr_new), kr_stride, _dtype_code(c_new), seq_ids.data_ptr(),
                                              positions.data_ptr(), n, _rope(64, rope_dim, base, interleaved),
                                              _raw_stream(c_new)))
@@ -541,6 +552,7 @@ def _latent_query(q_latent, q_rope, cache) -> _lib.LatentQuery:
     if q_latent.dim() != 3 or q_latent.shape[2] != 512:
         raise ValueError("q_latent must be [T, H, 512]")
     T, H, _ = q_latent.shape
+    _fit(T=T, H=H)
     st, sh, one = q_latent.stride()
     if q_latent.dtype is not torch.bfloat16:
         raise TypeError("q_latent must be bf16")
@@ -592,6 +604,8 @@ def dsa_sparse_attention(q_latent, q_rope, cache: LatentCache, page_table, seq_i
     k = idx.shape[1]
     _int32("seq_ids", seq_ids, T)
     _int32("idx", idx, T, k)
+    table = _page_table(page_table)
+    _fit(top_k=k)
     guard = _elsewhere(q_latent, stream)
     if guard is not None:
         with guard:
@@ -601,7 +615,7 @@ def dsa_sparse_attention(q_latent, q_rope, cache: LatentCache, page_table, seq_i
     out, lse, workspace, given = _outputs(T, H, q_latent, out, lse, workspace, need)
     _one_device(q_latent, cache.latent, cache.rope, cache.scale, page_table, seq_ids, idx, out, lse, workspace)
     _one_device(q_latent, q_rope, contiguous=False)
-    check(lib.dsa_sparse_attention(q, cache.c(), _page_table(page_table), seq_ids.data_ptr(), idx.data_ptr(), k, sm_scale,
+    check(lib.dsa_sparse_attention(q, cache.c(), table, seq_ids.data_ptr(), idx.data_ptr(), k, sm_scale,
                                    out.data_ptr(), lse.data_ptr(), _address(workspace), given, _raw_stream(q_latent)))
     return out, lse
 
@@ -620,14 +634,15 @@ def dsa_prefix_attention(q_latent, q_rope, cache: LatentCache, page_table, seq_i
     T, H = q.T, q.H
     _int32("seq_ids", seq_ids, T)
     _int32("key_lens", key_lens, T)
+    table = _page_table(page_table)
+    if max_keys is None:
+        max_keys = table.max_pages * cache.page_size
+    _fit(prefix_len=prefix_len, prefix_seq=prefix_seq, max_keys=max_keys)
     guard = _elsewhere(q_latent, stream)
     if guard is not None:
         with guard:
             return dsa_prefix_attention(q_latent, q_rope, cache, page_table, seq_ids, key_lens, sm_scale, prefix_len,
                                         prefix_seq, max_keys, out, lse, workspace)
-    table = _page_table(page_table)
-    if max_keys is None:
-        max_keys = table.max_pages * cache.page_size
     lib = _lib.load()
     need = 0 if workspace is not None else lib.dsa_prefix_attention_workspace_bytes(T, H, prefix_len, max_keys, cache.code)
     out, lse, workspace, given = _outputs(T, H, q_latent, out, lse, workspace, need)
@@ -640,10 +655,12 @@ def dsa_prefix_attention(q_latent, q_rope, cache: LatentCache, page_table, seq_i
 
 
 def dsa_sparse_attention_workspace_bytes(T: int, H: int, top_k: int, fp8: bool = False) -> int:
+    _fit(T=T, H=H, top_k=top_k)
     return int(_lib.load().dsa_sparse_attention_workspace_bytes(T, H, top_k, DSA_FP8_E4M3 if fp8 else DSA_BF16))
 
 
 def dsa_prefix_attention_workspace_bytes(T: int, H: int, prefix_len: int, max_keys: int, fp8: bool = False) -> int:
+    _fit(T=T, H=H, prefix_len=prefix_len, max_keys=max_keys)
     return int(_lib.load().dsa_prefix_attention_workspace_bytes(T, H, prefix_len, max_keys,
                                                                 DSA_FP8_E4M3 if fp8 else DSA_BF16))
 

@@ -7,8 +7,9 @@ import re
 import subprocess
 
 import pytest
+import torch
 
-from sparse_attention_token_02_b200 import build
+from sparse_attention_token_02_b200 import api, build
 
 
 def _sources():
@@ -62,7 +63,7 @@ def planner(tmp_path_factory):
     tmp = tmp_path_factory.mktemp("plan")
     (tmp / "fake.cpp").write_text(FAKE_DEVICE)
     cuda = os.path.join(os.path.dirname(os.path.dirname(build.nvcc())), "include")
-    subprocess.run(["g++", "-O1", "-std=c++17", "-fPIC", "-shared", f"-I{cuda}", f"-I{build.INCLUDE}", f"-I{build.CSRC}", "-x", "c++",
+    subprocess.run(["g++", "-O1", "-std=c++17", "-fPIC", "-shared", "-Wl,-Bsymbolic", f"-I{cuda}", f"-I{build.INCLUDE}", f"-I{build.CSRC}", "-x", "c++",
                     os.path.join(build.CSRC, "attention_plan.cu"), str(tmp / "fake.cpp"), "-o", str(tmp / "plan.so")], check=True)
     return ctypes.CDLL(str(tmp / "plan.so"))
 
@@ -83,3 +84,34 @@ def test_a_plan_without_the_devices_answer_is_not_kept(planner):
     assert planner.cluster_of(2, 128, 2048) == 1
     planner.set(0, 16, 0)
     assert planner.cluster_of(2, 128, 2048) > 1
+
+
+def test_numbers_that_do_not_fit_32_bits_are_refused():
+    # ctypes would pass their low 32 bits on: a rotation of 64 values for 2^32 + 64, a bound of 100 keys for 2^32 + 100
+    over = 2 ** 32
+    cache = api.LatentCache.empty(2, 64, device="cpu")
+    ids = torch.zeros(3, dtype=torch.int32)
+    table = torch.zeros(1, 2, dtype=torch.int32)
+    q, qr = torch.zeros(3, 4, 512, dtype=torch.bfloat16), torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="rope_dim must fit 32 bits"):
+        api.dsa_latent_append_rope(cache, table, torch.zeros(3, 512), torch.zeros(3, 64), ids, ids, rope_dim=over + 64)
+    for name in ("prefix_len", "prefix_seq", "max_keys"):
+        with pytest.raises(ValueError, match=f"{name} must fit 32 bits"):
+            api.dsa_prefix_attention(q, qr, cache, table, ids, ids, 0.1, **{name: over + 100})
+    wide = torch.zeros(1, 1, dtype=torch.int32).expand(1, 2 ** 26 + 1)          # pages of 64 rows: 2^32 positions and more
+    with pytest.raises(ValueError, match="max_keys must fit 32 bits"):
+        api.dsa_prefix_attention(q, qr, cache, wide, ids, ids, 0.1)
+    with pytest.raises(ValueError, match="max_pages must fit 32 bits"):
+        api.dsa_prefix_attention(q, qr, cache, torch.zeros(1, 1, dtype=torch.int32).expand(1, over + 1), ids, ids, 0.1, max_keys=64)
+    with pytest.raises(ValueError, match="top_k must fit 32 bits"):
+        api.dsa_sparse_attention(q, qr, cache, table, ids, torch.zeros(1, 1, dtype=torch.int32).expand(3, over + 1), 0.1)
+    one = torch.zeros(1, 1, 512, dtype=torch.bfloat16).expand(over + 3, 4, 512)
+    with pytest.raises(ValueError, match="T must fit 32 bits"):
+        api.dsa_sparse_attention(one, one[:, :, :64], cache, table, ids, ids, 0.1)
+    long = torch.empty(1, over + 16, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="d must fit 32 bits"):
+        api.dsa_rmsnorm_fp8(long, long[0])
+    with pytest.raises(ValueError, match="top_k must fit 32 bits"):
+        api.dsa_sparse_attention_workspace_bytes(1, 16, over + 64)
+    with pytest.raises(ValueError, match="prefix_len must fit 32 bits"):
+        api.dsa_prefix_attention_workspace_bytes(1, 16, over, 4096)
