@@ -16,10 +16,19 @@ import torch
 from . import _lib
 from ._lib import DSA_BF16, DSA_F32, DSA_FP8_E4M3, Batch, KCache, Query, check
 
-try:                                    # after torch, whose libraries it uses
-    from . import _layer_calls
-except ImportError:                     # not built, or for another torch: the Python forms below do the same
-    _layer_calls = None
+
+
+def _compiled_calls():
+    """The layer's compiled calls, or None where they are not built, or for another torch, whose C++ objects they
+    would read wrongly: the Python forms below do the same."""
+    try:                                # after torch, whose libraries it uses
+        from . import _layer_calls
+    except ImportError:
+        return None
+    return _layer_calls if getattr(_layer_calls, "torch_version", None) == torch.__version__ else None
+
+
+_layer_calls = _compiled_calls()
 
 
 def _ptr(t):

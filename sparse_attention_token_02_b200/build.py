@@ -6,8 +6,9 @@ Compiles every ``csrc/*.cu`` to an object with
 ``-gencode arch=compute_100a,code=sm_100a -lineinfo -O3`` and links them into
 ``libdsa_indexer.so`` next to this file (static CUDA runtime, so loading the
 library needs only the driver; only the ``dsa_*`` C symbols are exported).
-``csrc/layer_calls.cpp`` becomes ``_layer_calls.so``, the torch side of the layer's
-calls (g++, torch's headers).  Objects are rebuilt when a source or header is newer.
+``csrc/layer_calls.cpp`` becomes the module ``_layer_calls``, the torch side of the
+layer's calls (g++, torch's headers), for this Python and this torch.  Objects are rebuilt when a source or header is
+newer, the module also when its command (torch's version and place are in it) changes.
 """
 
 from __future__ import annotations
@@ -17,6 +18,7 @@ import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -28,7 +30,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdsa_indexer.so")
-CALLS = os.path.join(PKG, "_layer_calls.so")
+CALLS = os.path.join(PKG, "_layer_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+CALLS_COMMAND = os.path.join(BUILD, "layer_calls.command")   # what CALLS was built with
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -54,17 +57,48 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _calls_command(src: str) -> list[str] | None:
-    """None where torch or Python's headers are not there: the package then makes these calls from Python."""
-    spec, python = importlib.util.find_spec("torch"), sysconfig.get_paths()["include"]
-    if spec is None or not os.path.exists(os.path.join(python, "Python.h")):
+def _torch() -> tuple[str, str] | None:
+    """Where torch is and its version, without importing it."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
         return None
-    torch = spec.submodule_search_locations[0]
+    place = spec.submodule_search_locations[0]
+    with open(os.path.join(place, "version.py")) as f:
+        version = re.search(r"^__version__ = ['\"](.+?)['\"]", f.read(), re.M)
+    return (place, version.group(1)) if version else None
+
+
+def _calls_command(src: str) -> list[str] | None:
+    """None where torch or Python's headers are not there."""
+    found, python = _torch(), sysconfig.get_paths()["include"]
+    if found is None or not os.path.exists(os.path.join(python, "Python.h")):
+        return None
+    torch, version = found
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     dirs = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include/torch/csrc/api/include"),
             os.path.join(cuda, "include"), python]
-    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", *(f"-I{d}" for d in dirs), src, "-o", CALLS,
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", f'-DTORCH_BUILT_FOR="{version}"',
+            *(f"-I{d}" for d in dirs), src, "-o", CALLS,
             "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
+
+
+def _build_calls(run) -> None:
+    """The compiled calls, where they can be had: a module that no longer fits is taken away before it is built anew."""
+    src = os.path.join(CSRC, "layer_calls.cpp")
+    command = _calls_command(src)
+    wanted = " ".join(command or [])
+    if os.path.exists(CALLS_COMMAND) and not _stale(CALLS, [src] + _headers()):
+        with open(CALLS_COMMAND) as f:
+            if f.read() == wanted:
+                return
+    for old in (CALLS, CALLS_COMMAND):
+        if os.path.exists(old):
+            os.remove(old)
+    if command is None:
+        return
+    run(command)
+    with open(CALLS_COMMAND, "w") as f:
+        f.write(wanted)
 
 
 def build(jobs: int = 8, verbose: bool = False, extra: list[str] | None = None, out_dir: str | None = None) -> str:
@@ -91,11 +125,11 @@ def build(jobs: int = 8, verbose: bool = False, extra: list[str] | None = None, 
         if verbose and (r.stdout or r.stderr):
             print(r.stdout, r.stderr, flush=True)
 
-    calls = os.path.join(CSRC, "layer_calls.cpp")
-    command = _calls_command(calls) if not out_dir and _stale(CALLS, [calls] + headers) else None
-    shared = [command] if command else []
     with cf.ThreadPoolExecutor(max_workers=max(1, jobs)) as ex:
-        list(ex.map(run, shared + cmds))
+        calls = None if out_dir else ex.submit(_build_calls, run)
+        list(ex.map(run, cmds))
+        if calls is not None:
+            calls.result()
     if cmds or _stale(lib_path, objs):
         run([nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", lib_path, *objs])
     return lib_path

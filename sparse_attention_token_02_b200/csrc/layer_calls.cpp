@@ -326,4 +326,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer_calls", nullptr, -1, method
 
 }  // namespace
 
-extern "C" PyMODINIT_FUNC PyInit__layer_calls() { return PyModule_Create(&module); }
+// TORCH_BUILT_FOR: the version of torch whose headers these are
+extern "C" PyMODINIT_FUNC PyInit__layer_calls() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_BUILT_FOR) < 0) Py_CLEAR(m);
+  return m;
+}

@@ -2,6 +2,7 @@
 
 import ctypes
 import glob
+import importlib.machinery
 import os
 import re
 import subprocess
@@ -115,3 +116,35 @@ def test_numbers_that_do_not_fit_32_bits_are_refused():
         api.dsa_sparse_attention_workspace_bytes(1, 16, over + 64)
     with pytest.raises(ValueError, match="prefix_len must fit 32 bits"):
         api.dsa_prefix_attention_workspace_bytes(1, 16, over, 4096)
+
+
+@pytest.fixture
+def calls_at(tmp_path, monkeypatch):
+    """Builds of the compiled calls go to another place."""
+    path = str(tmp_path / "_layer_calls.so")
+    monkeypatch.setattr(build, "CALLS", path)
+    monkeypatch.setattr(build, "CALLS_COMMAND", str(tmp_path / "command"))
+    return path
+
+
+def test_compiled_calls_follow_torchs_version(calls_at, monkeypatch):
+    made = []
+
+    def run(command):
+        made.append(command)
+        with open(calls_at, "w") as f:
+            f.write("module")
+
+    for _ in range(2):                                       # the second finds it as it should be
+        build._build_calls(run)
+    assert len(made) == 1 and any(torch.__version__ in part for part in made[0])
+    place, version = build._torch()
+    monkeypatch.setattr(build, "_torch", lambda: (place, "0.0"))
+    build._build_calls(run)
+    assert len(made) == 2
+
+
+def test_compiled_calls_for_another_torch_are_declined(monkeypatch):
+    assert build.CALLS.endswith(importlib.machinery.EXTENSION_SUFFIXES[0])
+    monkeypatch.setattr(torch, "__version__", "0.0")
+    assert api._compiled_calls() is None
