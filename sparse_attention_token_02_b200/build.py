@@ -7,7 +7,8 @@ Compiles every ``csrc/*.cu`` to an object with
 ``libdsa_indexer.so`` next to this file (static CUDA runtime, so loading the
 library needs only the driver; only the ``dsa_*`` C symbols are exported).
 ``csrc/layer_calls.cpp`` becomes the module ``_layer_calls``, the torch side of the
-layer's calls (g++, torch's headers), for this Python and this torch.  Objects are rebuilt when a source or header is
+layer's calls (g++, torch's headers), for this Python and this torch; the package does
+without it where it cannot be built.  Objects are rebuilt when a source or header is
 newer, the module also when its command (torch's version and place are in it) changes.
 """
 
@@ -96,7 +97,11 @@ def _build_calls(run) -> None:
             os.remove(old)
     if command is None:
         return
-    run(command)
+    try:
+        run(command)
+    except (RuntimeError, OSError) as e:                     # no g++, a torch without CUDA, ...
+        print(f"the layer's compiled calls could not be built, its Python forms serve instead: {e}", file=sys.stderr)
+        return
     with open(CALLS_COMMAND, "w") as f:
         f.write(wanted)
 

@@ -127,6 +127,15 @@ def calls_at(tmp_path, monkeypatch):
     return path
 
 
+def test_compiled_calls_that_cannot_be_built_are_done_without(calls_at, monkeypatch, capsys):
+    with open(calls_at, "w") as f:
+        f.write("of an earlier build")
+    for command in (["g++", "--no-such-flag"], ["no-such-compiler"], None):
+        monkeypatch.setattr(build, "_calls_command", lambda src, command=command: command)
+        assert os.path.exists(build.build()) and not os.path.exists(calls_at)
+        assert (command is None) == ("Python forms" not in capsys.readouterr().err)
+
+
 def test_compiled_calls_follow_torchs_version(calls_at, monkeypatch):
     made = []
 
