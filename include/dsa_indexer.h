@@ -392,7 +392,8 @@ DSA_API dsa_status_t dsa_sort_selection(int32_t* idx, float* score, int64_t rows
  *                short); 0: one scale per row, scale [rows], as dsa_quantize_rows_fp8
  *   normed       device [rows, d] bf16: y itself as well, or NULL
  * d: a positive multiple of 16, at most 32768.  All pointers and rows 16-byte aligned (scale: 4).
- * A NaN or infinity in a row spoils that row only.
+ * A NaN or infinity in a row spoils that row only; sums s may be as large as fp32 holds, for weights below 2^70.
+ * Squares are fp32: below 2^-149 they count as nothing beside eps, which should then be above it.
  */
 DSA_API dsa_status_t dsa_rmsnorm_fp8(const void* x, dsa_dtype_t dtype, int64_t x_stride, const void* residual,
                                      void* residual_out, const void* weight, dsa_dtype_t weight_dtype, int64_t rows,

@@ -16,6 +16,8 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import e4m3_decode
+from oracle import layer as L
 from sparse_attention_token_02_b200 import _lib, api
 from .test_gpu_layer import SM, check_token, f64, gen, make_cache, queries
 
@@ -188,3 +190,33 @@ def test_what_is_only_read_is_not_copied_first():
     r = subprocess.run([sys.executable, "-c", LAZY], capture_output=True, text=True, timeout=300,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and "equal" in r.stdout, (r.returncode, r.stdout, r.stderr[-2000:])
+
+
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("d", [384, 4112, 16384])
+@pytest.mark.parametrize("mag,weight,residual", [(2.0 ** 126, 40.0, True), (2.0 ** 127, 2.0 ** 60, False), (2.0 ** 100, 2.0 ** -60, False),
+                                                 (2.0 ** 47, 1.0, True)])
+def test_norm_whose_weighted_values_would_overflow(mag, weight, residual, d, group):
+    # s * weight is past fp32 where the normed value is not: whole rows of such values, and groups of them beside
+    # ordinary and small ones.  Bounds as for every norm, half a step of subnormal numbers with them.
+    x = (torch.rand(5, d, generator=gen(7)) / 2 + 0.25) * torch.sign(torch.randn(5, d, generator=gen(8)))
+    res = x.flip(0) / 2 if residual else None
+    w = weight * (torch.rand(d, generator=gen(9)) + 0.5)
+    unit = torch.ones(5, d)
+    unit[0] = mag
+    unit[1, 128:256] = mag
+    unit[2, :128], unit[2, 256:] = mag, 2.0 ** -40
+    unit[3, 5] = mag
+    x = x * unit
+    res = res * unit if residual else None
+    normed = torch.empty(5, d, dtype=torch.bfloat16, device="cuda")
+    codes, scale, _ = api.dsa_rmsnorm_fp8(x.cuda(), w.cuda(), 1e-6, residual=res.cuda() if residual else None, group=group, normed=normed)
+    s, y = L.rmsnorm(f64(x), f64(w), 1e-6, f64(res) if residual else None)
+    ref = L.group_scales(y, group)
+    # fp32 holds nothing below 2^-149: a group whose y are smaller is one of zeros (at most half of that rounds up)
+    zeros = (448 * ref < 2.0 ** -149) & (f64(scale) == 1)
+    assert np.all(zeros | (np.abs(f64(scale) - ref) <= 2.0 ** -18 * ref + 2.0 ** -149))
+    assert np.all(np.abs(f64(normed) - y) <= (2.0 ** -8 + 2.0 ** -17) * np.abs(y) + 2.0 ** -134)
+    wide = np.repeat(f64(scale), group or d, axis=1)[:, :d]
+    got = e4m3_decode(codes.cpu().numpy()) * wide
+    assert np.all(np.abs(got - y) <= np.maximum(2.0 ** -4 * np.abs(y), 2.0 ** -10 * wide) + 2.0 ** -17 * np.abs(y) + 448 * 2.0 ** -149)
