@@ -403,7 +403,8 @@ DSA_API dsa_status_t dsa_rmsnorm_fp8(const void* x, dsa_dtype_t dtype, int64_t x
 /* The paged latent cache of one layer: num_pages pages of page_size rows, a row per token. */
 typedef struct {
   void* latent;           /* device [num_pages * page_size, d_c] bf16 or E4M3 codes, 16-byte aligned     */
-  float* scale;           /* device [num_pages * page_size] fp32, a power of two per row (FP8), else NULL */
+  float* scale;           /* device [num_pages * page_size] fp32, a power of two per row (FP8), else NULL;
+                             with another scale attention reads code * scale rounded to bf16             */
   void* rope;             /* device [num_pages * page_size, d_r] bf16, 16-byte aligned; NULL for d_r = 0  */
   int32_t num_pages;
   int32_t page_size;      /* any positive size; num_pages * page_size < 2^31                             */

@@ -379,7 +379,9 @@ def dsa_sort_selection(idx, score, stream=None):
 @dataclass
 class LatentCache:
     """A paged latent cache: ``latent`` [pages * page_size, 512] bf16 or uint8 (E4M3 codes), ``rope``
-    [pages * page_size, 64] bf16 (None: no rotated key part), ``scale`` [pages * page_size] fp32 (FP8)."""
+    [pages * page_size, 64] bf16 (None: no rotated key part), ``scale`` [pages * page_size] fp32 (FP8): a power of two
+    per row, as the append writes it.  Attention multiplies in bf16, in which code times such a scale is exact; with
+    any other scale it reads the bf16 nearest to the product, half a step (2^-8) off at most."""
     latent: torch.Tensor
     rope: torch.Tensor | None
     scale: torch.Tensor | None = None

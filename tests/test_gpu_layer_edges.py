@@ -220,3 +220,26 @@ def test_norm_whose_weighted_values_would_overflow(mag, weight, residual, d, gro
     wide = np.repeat(f64(scale), group or d, axis=1)[:, :d]
     got = e4m3_decode(codes.cpu().numpy()) * wide
     assert np.all(np.abs(got - y) <= np.maximum(2.0 ** -4 * np.abs(y), 2.0 ** -10 * wide) + 2.0 ** -17 * np.abs(y) + 448 * 2.0 ** -149)
+
+
+@pytest.mark.parametrize("T,H,prefix,own", [(3, 16, 300, 40), (40, 16, 8000, 30)])
+def test_fp8_scales_of_another_writer(T, H, prefix, own):
+    # scales that are not powers of two: every value is the bf16 nearest to code times scale, expanded once or on the way
+    page, full = 64, prefix // 64
+    pages = full + 2
+    num_pages = full + 2 * T
+    cache, vals = make_cache(num_pages * page, page, True, T)
+    scale = torch.rand(num_pages * page, generator=gen(3)) / 100 + 0.002
+    cache.scale.copy_(scale)
+    latent = e4m3_decode(cache.latent.cpu().numpy()) * f64(scale)[:, None]
+    vals[:, :512] = f64(torch.from_numpy(latent).float().bfloat16())
+    table = torch.cat([torch.arange(full).expand(T, full), full + torch.arange(2 * T).view(T, 2)], 1).to(torch.int32)
+    lens = torch.full((T,), prefix + own, dtype=torch.int32)
+    ql, qr = queries(T, H, 7)
+    out, lse = api.dsa_prefix_attention(ql.cuda(), qr.cuda(), cache, table.cuda(), torch.arange(T, dtype=torch.int32).cuda(), lens.cuda(),
+                                        SM, prefix_len=full * page, max_keys=prefix + own)
+    api.dsa_check_device_errors()
+    q = f64(torch.cat([ql, qr], 2))
+    for t in (0, 1, T - 1):
+        rows = [L.page_row(table.numpy(), page, num_pages, t, p) for p in range(prefix + own)]
+        check_token(f64(out)[t], f64(lse)[t], q[t], vals[rows], SM, t)
