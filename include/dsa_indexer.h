@@ -459,7 +459,7 @@ typedef struct {
  *            selection from prefill or decode); a position named twice counts twice
  *   out      device [T, H, 512] bf16, contiguous, 16-byte aligned
  *   lse      device fp32 [T, H] or NULL
- *   sm_scale positive and finite
+ *   sm_scale positive, at most 2^127
  * A token with no entry, or with a negative sequence (padding), gets zeros and -inf.  Scores, softmax
  * statistics and sums are fp32; the weights are rounded to bf16 for their product with the latents.  The
  * result is the same, bit for bit, on every run.

@@ -1389,6 +1389,7 @@ dsa_status_t run_attention(const dsa_latent_query_t* q, AttnArgs* a, int64_t sha
   if (!out) return fail(DSA_ERR_INVALID_ARG, "out is NULL");
   if (!aligned16(out)) return fail(DSA_ERR_INVALID_ARG, "out must be 16-byte aligned");
   if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return fail(DSA_ERR_INVALID_ARG, "sm_scale must be positive and finite");
+  if (!(sm_scale <= 0x1p127f)) return fail(DSA_ERR_INVALID_ARG, "sm_scale must be at most 2^127");   // times log2(e) finite
   a->q_latent = q->latent;
   a->ql_t = q->latent_stride_t;
   a->ql_h = q->latent_stride_h;

@@ -10,7 +10,7 @@ import subprocess
 import pytest
 import torch
 
-from sparse_attention_token_02_b200 import api, build
+from sparse_attention_token_02_b200 import _lib, api, build
 
 
 def _sources():
@@ -157,3 +157,18 @@ def test_compiled_calls_for_another_torch_are_declined(monkeypatch):
     assert build.CALLS.endswith(importlib.machinery.EXTENSION_SUFFIXES[0])
     monkeypatch.setattr(torch, "__version__", "0.0")
     assert api._compiled_calls() is None
+
+
+def test_a_softmax_scale_that_overflows_in_base_2_is_refused():
+    # scores are held times log2(e): 2^127.5 times it is past fp32, and 0 times infinity a NaN
+    lib = _lib.load()
+    cache = _lib.LatentCacheView(0x100000, None, 0x200000, 8, 64, 512, 64, _lib.DSA_BF16)
+    table, q = _lib.PageTable(0x300000, 2, 4), _lib.LatentQuery(0x400000, 65536, 512, 0x500000, 8192, 64, 4, 128)
+    P = ctypes.c_void_p
+    for scale in (2.0 ** 127.5, 3.4e38):
+        got = [lib.dsa_sparse_attention(ctypes.byref(q), ctypes.byref(cache), ctypes.byref(table), P(0x600000), P(0x700000), 16, scale,
+                                        P(0x800000), None, None, 0, None),
+               lib.dsa_prefix_attention(ctypes.byref(q), ctypes.byref(cache), ctypes.byref(table), P(0x600000), P(0x700000), 4, 0, 16,
+                                        scale, P(0x800000), None, None, 0, None)]
+        assert [_lib.STATUS_NAMES[s] for s in got] == ["DSA_ERR_INVALID_ARG"] * 2
+        assert b"sm_scale" in lib.dsa_get_last_error()
