@@ -39,7 +39,7 @@ AttnPlan make_plan(int64_t T, int32_t H, int64_t shared_keys, int64_t own_keys, 
   int64_t shared_tiles = ceil_div(shared_keys, kAttnTile);
   // Expanding FP8 rows to bf16 costs the loading warps more time than a tile's products take; a prefix that many
   // groups of rows read is expanded once instead (23 x 128 heads over 16001 keys: 248 -> 173 us
-  // then, 147 in pairs).
+  // then, 151 in pairs).
   const bool expand = fp8 && shared_groups >= 4 && shared_groups * shared_tiles >= 8 * sms;
   if (H % kAttnRows == 0 && !expand) {
     own_keys += shared_keys;

@@ -789,8 +789,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(AttnArgs a, Attn
 // of 576 values), for the second product half of the values of all its keys (64 rows of 256).  Keys and values have
 // their own stages: a tile's keys are free after its scores, its values after the second product.  CTA 0 issues; CTA 1's
 // two idle warps tell it when their CTA's keys and values have landed.  (64 x 128 heads over 2048 selected keys 69 us with
-// one CTA per 64 rows, 56 in pairs; 1024 tokens 805 and 687.)  A tile takes about 1800 cycles: 1280 of products, about 1500 of shared memory (operands
-// 860, copies in 540, weights 100).  Copying the values of a CTA's own keys from its keys' stage, which spares a quarter
+// one CTA per 64 rows, 55 in pairs; 1024 tokens 805 and 687 to 700.)  With the keys in L2 a tile takes about 1800 cycles: 1280 of
+// products, about 1500 of shared memory (operands 860, copies in 540, weights 100); neither is busy throughout, and the
+// rest goes to the hand-overs between loads, products and weights.  Copying the values of a CTA's own keys from its keys' stage, which spares a quarter
 // of the reads of L2, cost 743 us for the 703 of then; a third stage of keys for one of values changed nothing.
 constexpr uint32_t kPairKeys = (kLatentBlocks + 1) * 4096u;  // 32 rows x 9 blocks
 constexpr uint32_t kPairValues = 4 * kBlock;                 // 64 rows x 4 blocks

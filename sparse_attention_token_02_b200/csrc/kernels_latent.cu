@@ -12,9 +12,10 @@
 // product gives the angle's fraction of a turn at any position (within p * 2^-53, as in fp64, and 2^-31), and sine and
 // cosine of a fraction of a turn need no reduction.
 // Bound by HBM (about 1.2 KB read and 0.7 to 1.2 KB written a token); one warp per token with all its loads issued
-// before the first use, even of the token's sequence.  16384 tokens to FP8, back to back in a graph: 12.5 us with fp64
-// angles and the sequence awaited first, 8.25 now (3.6 TB/s); the frequencies go through shared memory because a warp
-// whose lanes read different parameters is served lane by lane (9.9 us).  32 tokens: 1.6 us.
+// before the first use, even of the token's sequence.  16384 tokens to FP8, back to back in a graph over four sets of
+// tensors: 12.5 us with fp64 angles and the sequence awaited first, 8.0 now (3.7 TB/s, 8.3 over more sets; 5.8 to 6.2 where up
+// to three sets, 30 MB each, stay in the L2); the frequencies go through shared memory because a warp whose lanes read
+// different parameters is served lane by lane (9.9 us).  32 tokens: 1.6 us.
 #include <cuda_bf16.h>
 
 #include <cmath>

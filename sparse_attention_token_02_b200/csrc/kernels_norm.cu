@@ -13,7 +13,7 @@
 // with 1 / 448 within one more.
 //
 // Bound by HBM: each input is read and each output written once (7 bytes a value for bf16 with a residual); 16384 x 7168
-// rows back to back in a graph take 130 us (97 % of the measured copy rate), without a residual 94 us (58 %: there the
+// rows back to back in a graph take 129 us (98 % of the measured copy rate), without a residual 91 to 94 us (59 %: there the
 // instructions, some 20 a value, weigh as much).  A CTA keeps a row in registers between the sum and the codes and has
 // its next row's loads under way meanwhile: one CTA a row and weights applied after the sum took 133 and 107 us, and
 // 17 us for 16384 rows of 128 values that take 6 now.  A ring of rows in shared memory (155 us) cost more than it hid.
