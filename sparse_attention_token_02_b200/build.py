@@ -61,9 +61,11 @@ def _stale(target: str, deps: list[str]) -> bool:
 def _torch() -> tuple[str, str] | None:
     """Where torch is and its version, without importing it."""
     spec = importlib.util.find_spec("torch")
-    if spec is None:
+    if spec is None or not spec.submodule_search_locations:
         return None
     place = spec.submodule_search_locations[0]
+    if not os.path.exists(os.path.join(place, "version.py")):
+        return None
     with open(os.path.join(place, "version.py")) as f:
         version = re.search(r"^__version__ = ['\"](.+?)['\"]", f.read(), re.M)
     return (place, version.group(1)) if version else None

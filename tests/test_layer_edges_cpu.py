@@ -3,6 +3,7 @@
 import ctypes
 import glob
 import importlib.machinery
+import importlib.util
 import os
 import re
 import subprocess
@@ -151,6 +152,13 @@ def test_compiled_calls_follow_torchs_version(calls_at, monkeypatch):
     monkeypatch.setattr(build, "_torch", lambda: (place, "0.0"))
     build._build_calls(run)
     assert len(made) == 2
+
+
+def test_a_torch_that_names_no_version_is_no_torch_to_build_for(calls_at, tmp_path, monkeypatch):
+    spec = importlib.machinery.ModuleSpec("torch", None, is_package=True)
+    spec.submodule_search_locations.append(str(tmp_path))
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name: spec)
+    assert build._torch() is None and build._calls_command("layer_calls.cpp") is None
 
 
 def test_compiled_calls_for_another_torch_are_declined(monkeypatch):
