@@ -1303,7 +1303,8 @@ const char* dsa_version(void) { return "dsa_indexer 0.1 (sm_100a)"; }
 namespace dsa {
 namespace {
 
-bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool aligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+bool aligned16(const void* p) { return aligned(p, 16); }
 
 dsa_status_t check_latent(const dsa_latent_cache_t* c, const dsa_page_table_t* t, LatentView* v) {
   if (!c || !t) return fail(DSA_ERR_INVALID_ARG, "latent cache or page table is NULL");
@@ -1318,6 +1319,8 @@ dsa_status_t check_latent(const dsa_latent_cache_t* c, const dsa_page_table_t* t
     return fail(DSA_ERR_INVALID_ARG, "num_pages and page_size must be positive and hold fewer than 2^31 rows");
   if (t->num_seqs < 1 || t->max_pages < 1) return fail(DSA_ERR_INVALID_ARG, "page table must have at least one row and one column");
   if (!aligned16(c->latent) || !aligned16(c->rope)) return fail(DSA_ERR_INVALID_ARG, "latent and rope must be 16-byte aligned");
+  if ((c->dtype == DSA_FP8_E4M3 && !aligned(c->scale, 4)) || !aligned(t->pages, 4))
+    return fail(DSA_ERR_INVALID_ARG, "scale and pages must be 4-byte aligned");
   *v = LatentView{c->latent, c->dtype == DSA_FP8_E4M3 ? c->scale : nullptr, c->d_r ? c->rope : nullptr, c->num_pages,
                   c->page_size, c->page_size & (c->page_size - 1) ? -1 : __builtin_ctz(c->page_size), c->dtype == DSA_FP8_E4M3, t->pages, t->num_seqs, t->max_pages};
   return DSA_OK;
@@ -1388,6 +1391,8 @@ dsa_status_t run_attention(const dsa_latent_query_t* q, AttnArgs* a, int64_t sha
                            void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream_v) {
   if (!out) return fail(DSA_ERR_INVALID_ARG, "out is NULL");
   if (!aligned16(out)) return fail(DSA_ERR_INVALID_ARG, "out must be 16-byte aligned");
+  if (!aligned(a->seq_ids, 4) || !aligned(a->idx, 4) || !aligned(a->key_lens, 4) || !aligned(lse, 4))
+    return fail(DSA_ERR_INVALID_ARG, "seq_ids, idx, key_lens and lse must be 4-byte aligned");
   if (!(sm_scale > 0.f) || !std::isfinite(sm_scale)) return fail(DSA_ERR_INVALID_ARG, "sm_scale must be positive and finite");
   if (!(sm_scale <= 0x1p127f)) return fail(DSA_ERR_INVALID_ARG, "sm_scale must be at most 2^127");   // times log2(e) finite
   a->q_latent = q->latent;
@@ -1447,6 +1452,7 @@ dsa_status_t dsa_rmsnorm_fp8(const void* x, dsa_dtype_t dtype, int64_t x_stride,
   if (!aligned16(x) || (rows > 1 && x_stride * esz % 16) || !aligned16(residual) || !aligned16(residual_out) ||
       !aligned16(weight) || !aligned16(codes) || !aligned16(normed))
     return fail(DSA_ERR_INVALID_ARG, "rows, weight, codes and normed must be 16-byte aligned");
+  if (!aligned(scale, 4)) return fail(DSA_ERR_INVALID_ARG, "scale must be 4-byte aligned");
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
   Ctx* c = nullptr;
   dsa_status_t st = get_ctx(stream, &c);
@@ -1482,6 +1488,8 @@ dsa_status_t dsa_latent_append_rope(const dsa_latent_cache_t* cache, const dsa_p
   const int64_t esz = src_dtype == DSA_F32 ? 4 : 2;
   if (!aligned16(c_new) || (n > 1 && c_stride * esz % 16))
     return fail(DSA_ERR_INVALID_ARG, "rows of c_new must be 16-byte aligned");
+  if ((a.kv.rope && !aligned(kr_new, static_cast<size_t>(esz))) || !aligned(seq_ids, 4) || !aligned(positions, 4))
+    return fail(DSA_ERR_INVALID_ARG, "kr_new, seq_ids and positions must be aligned to their values");
   if (n > 1 && (c_stride < kLatentDim || (a.kv.rope && kr_stride < kLatentRope)))
     return fail(DSA_ERR_INVALID_ARG, "row strides must be at least the row lengths");
   a.c_new = c_new;

@@ -180,3 +180,34 @@ def test_a_softmax_scale_that_overflows_in_base_2_is_refused():
                                         scale, P(0x800000), None, None, 0, None)]
         assert [_lib.STATUS_NAMES[s] for s in got] == ["DSA_ERR_INVALID_ARG"] * 2
         assert b"sm_scale" in lib.dsa_get_last_error()
+
+
+def test_pointers_that_are_not_aligned_to_their_values_are_refused():
+    # a device fault otherwise; torch's tensors are always aligned, other callers' buffers may not be
+    lib, P = _lib.load(), ctypes.c_void_p
+    bad = []
+
+    def norm(scale=0x60000):
+        return lib.dsa_rmsnorm_fp8(P(0x10000), _lib.DSA_BF16, 256, None, None, P(0x40000), _lib.DSA_BF16, 4, 256, 1e-6, 128, P(0x50000),
+                                   P(scale), None, None)
+
+    def append(scale=0x900000, pages=0x300000, kr=0x700000, seq=0x600000, pos=0x800000, dtype=_lib.DSA_F32):
+        cache = _lib.LatentCacheView(0x100000, scale, 0x200000, 8, 64, 512, 64, _lib.DSA_FP8_E4M3)
+        return lib.dsa_latent_append_rope(ctypes.byref(cache), ctypes.byref(_lib.PageTable(pages, 2, 4)), P(0xA00000), 512, P(kr), 64, dtype,
+                                          P(seq), P(pos), 4, ctypes.byref(_lib.Rope(64, 1, 10000.0)), None)
+
+    def attention(prefix, seq=0x600000, keys=0x700000, lse=0x900000):
+        cache, table = _lib.LatentCacheView(0x100000, None, 0x200000, 8, 64, 512, 64, _lib.DSA_BF16), _lib.PageTable(0x300000, 2, 4)
+        q = _lib.LatentQuery(0x400000, 65536, 512, 0x500000, 8192, 64, 4, 128)
+        args = [ctypes.byref(q), ctypes.byref(cache), ctypes.byref(table), P(seq), P(keys)]
+        args += [4, 0, 16] if prefix else [16]
+        return (lib.dsa_prefix_attention if prefix else lib.dsa_sparse_attention)(*args, 0.1, P(0x800000), P(lse), None, 0, None)
+
+    for call, name, at in ((norm, "scale", 0x60002), (append, "scale", 0x900002), (append, "pages", 0x300002), (append, "kr", 0x700002),
+                           (append, "seq", 0x600001), (append, "pos", 0x800002)):
+        bad.append((name, call(**{name: at}), lib.dsa_get_last_error()))
+    for prefix in (False, True):
+        for name, at in (("seq", 0x600002), ("keys", 0x700001), ("lse", 0x900002)):
+            bad.append((name, attention(prefix, **{name: at}), lib.dsa_get_last_error()))
+    assert append(kr=0x700001, dtype=_lib.DSA_BF16) == 1
+    assert all(status == 1 and b"aligned" in message for _, status, message in bad), bad     # DSA_ERR_INVALID_ARG
